@@ -32,6 +32,15 @@ FATHOM_SCAN_DEFAULT = 0
 FATHOM_SCAN_FORCE_EXACT = 1
 FATHOM_SCAN_PROFILE = 2
 
+FATHOM_F32 = 0
+FATHOM_BF16 = 1
+FATHOM_F16 = 2
+
+FATHOM_ROTARY_PLAIN = 0
+FATHOM_ROTARY_LINEAR = 1
+FATHOM_ROTARY_NTK = 2
+FATHOM_ROTARY_YARN = 3
+
 EXPORTED = (
     "fathom_n_words", "fathom_status_str", "fathom_pack_workspace_bytes", "fathom_pack_keys",
     "fathom_plan", "fathom_fixed_plan", "fathom_scan_workspace_bytes", "fathom_scan_topk",
@@ -40,6 +49,9 @@ EXPORTED = (
     "fathom_scan_topk_static", "fathom_link_probe", "fathom_append_keys",
     "fathom_sparse_attention_workspace_bytes", "fathom_sparse_attention", "fathom_plan_marginal",
     "fathom_merge_topk",
+    "fathom_rotary_turns", "fathom_qk_norm_rope", "fathom_append_kv",
+    "fathom_paged_attention_workspace_bytes", "fathom_paged_attention",
+    "fathom_sparse_attention_paged_workspace_bytes", "fathom_sparse_attention_paged",
 )
 
 
@@ -62,6 +74,32 @@ class fathom_index(ctypes.Structure):
     ]
 
 
+class fathom_rows(ctypes.Structure):
+    """Mirror of the C fathom_rows view."""
+    _fields_ = [
+        ("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("n_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
+class fathom_rotary(ctypes.Structure):
+    """Mirror of the C fathom_rotary descriptor."""
+    _fields_ = [
+        ("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+    ]
+
+
+class fathom_kv_cache(ctypes.Structure):
+    """Mirror of the C fathom_kv_cache descriptor."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -76,6 +114,9 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P, I32, SZ, U32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_uint32
     IX = ctypes.POINTER(fathom_index)
+    RW, RO = ctypes.POINTER(fathom_rows), ctypes.POINTER(fathom_rotary)
+    KV, F32, F64, I64 = (ctypes.POINTER(fathom_kv_cache), ctypes.c_float, ctypes.c_double,
+                         ctypes.c_int64)
     sig = {
         "fathom_n_words": ([I32], I32),
         "fathom_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -99,6 +140,15 @@ def load_library(path: str = LIB_PATH):
         "fathom_link_probe": ([P, SZ, P, P], ctypes.c_int),
         "fathom_profile_read": ([ctypes.POINTER(ctypes.c_double),
                                  ctypes.POINTER(ctypes.c_uint64)], ctypes.c_int),
+        "fathom_rotary_turns": ([P, P, I32, F64, I32, F64, I64, F64, F64], ctypes.c_int),
+        "fathom_qk_norm_rope": ([I32, I32, P, RO, P, P, F32, RW, RW, RW, RW, P], ctypes.c_int),
+        "fathom_append_kv": ([KV, I32, RW, RW, P, P, P, I32, I32, RO, P, F32, P], ctypes.c_int),
+        "fathom_paged_attention_workspace_bytes": ([KV, I32, I32, I32, I32], SZ),
+        "fathom_paged_attention": ([KV, RW, P, I32, P, I32, I32, I32, F32, F32, P, RW, P, SZ, P],
+                                   ctypes.c_int),
+        "fathom_sparse_attention_paged_workspace_bytes": ([I32, I32, I32, I32], SZ),
+        "fathom_sparse_attention_paged": ([KV, RW, P, I32, P, I32, P, I32, F32, F32, P, RW, P, SZ,
+                                           P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -256,6 +306,190 @@ def fathom_merge_topk(shard_idx, shard_score, shard_offset, k: int, out_idx, out
                                             _stream(stream)), "fathom_merge_topk")
 
 
+# ------------------------------------------------- calls on a paged cache
+# These take tensors, whose shapes and strides they pass on.  A tensor that the
+# C call would misread (wrong type, layout or device) raises ValueError.  The
+# call runs on the tensors' device, on `stream` or that device's current one.
+_DTYPES = {}
+
+
+def _dtype_code(dtype) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: FATHOM_F32, torch.bfloat16: FATHOM_BF16,
+                        torch.float16: FATHOM_F16})
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"float32, bfloat16 or float16 rows are wanted, not {dtype}")
+    return code
+
+
+def _rows(x, what: str) -> fathom_rows:
+    """View of a CUDA tensor [tokens][heads][channels]."""
+    if x.dim() != 3 or not x.is_cuda or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError(f"{what}: a CUDA tensor [tokens][heads][channels] with contiguous "
+                         "channels is wanted")
+    return fathom_rows(x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], _dtype_code(x.dtype))
+
+
+def _dense(x, what: str, dtype: str, shape, device) -> int:
+    """Address of a contiguous device tensor of the given type and shape."""
+    if str(x.dtype)[6:] != dtype or tuple(x.shape) != tuple(shape) or x.device != device \
+            or not x.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor {tuple(shape)} on {device} is "
+                         f"wanted, not {str(x.dtype)[6:]} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def _same_shape(x, y, what: str):
+    if x.shape != y.shape or x.device != y.device:
+        raise ValueError(f"{what}: {tuple(y.shape)} on {y.device} does not fit "
+                         f"{tuple(x.shape)} on {x.device}")
+
+
+def _weight(w, rows, what: str) -> int:
+    if w is None:
+        return 0
+    return _dense(w, what, str(rows.dtype)[6:], rows.shape[2:], rows.device)
+
+
+def _run_on(device, stream, what: str, call):
+    """call(stream handle) with `device` current; raises on an error status."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        rc = call(_stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = call(_stream(stream))
+    if rc != FATHOM_OK:
+        raise FathomError(rc, what)
+
+
+def _rotary_ref(rotary, device):
+    if rotary is None:
+        return None
+    if rotary.device != device:
+        raise ValueError(f"rotary table on {rotary.device}, rows on {device}")
+    return ctypes.byref(rotary.desc)
+
+
+def fathom_rotary_turns(rotary_dim: int, base: float = 10000.0, scaling: int = FATHOM_ROTARY_PLAIN,
+                        factor: float = 1.0, original_len: int = 1, beta_fast: float = 32.0,
+                        beta_slow: float = 1.0):
+    """-> (list of rotary_dim/2 turns per position, magnitude)."""
+    turns = (ctypes.c_double * max(1, int(rotary_dim) // 2))()
+    magnitude = ctypes.c_float()
+    _check(load_library().fathom_rotary_turns(turns, ctypes.byref(magnitude), int(rotary_dim),
+                                              float(base), int(scaling), float(factor),
+                                              int(original_len), float(beta_fast),
+                                              float(beta_slow)), "fathom_rotary_turns")
+    return list(turns), magnitude.value
+
+
+def fathom_qk_norm_rope(q, k, pos, q_out, k_out, rotary=None, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, stream=None):
+    """Norm (where a weight is given) and rotation (where a RotaryTable is
+    given) of query rows q [T][Hq][d] and key rows k [T][Hk][d] at positions
+    pos (int32 [T]) into q_out and k_out; q and q_out, or k and k_out, may be
+    None."""
+    lead = q if q is not None else k
+    if lead is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q with q_out, k with k_out, or both are wanted")
+    rows = []
+    for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            rows += [None, None]
+            continue
+        if x.shape[0] != lead.shape[0] or x.shape[2] != lead.shape[2] or x.device != lead.device:
+            raise ValueError("q and k differ in tokens, channels or device")
+        _same_shape(x, out, what + "_out")
+        rows += [ctypes.byref(_rows(x, what)), ctypes.byref(_rows(out, what + "_out"))]
+    n = lead.shape[0]
+    at = 0 if pos is None else _dense(pos, "pos", "int32", (n,), lead.device)
+    wq = 0 if q is None else _weight(q_weight, q, "q_weight")
+    wk = 0 if k is None else _weight(k_weight, k, "k_weight")
+    table = _rotary_ref(rotary, lead.device)
+    fn = load_library().fathom_qk_norm_rope
+    _run_on(lead.device, stream, "fathom_qk_norm_rope",
+            lambda s: fn(n, lead.shape[2], at, table, wq, wk, eps, *rows, s))
+
+
+def fathom_append_kv(cache: fathom_kv_cache, k, v, seq, pos, page_table, rotary=None,
+                     k_weight=None, eps: float = 1e-6, stream=None):
+    """Write key rows k and value rows v [T][H][d] to positions pos (int32 [T])
+    of sequences seq (int32 [T], negative: padding) of a paged cache, each key
+    normed and rotated on the way; page_table int32 [n_seqs][pages]."""
+    _same_shape(k, v, "v")
+    if k.shape[-1] != cache.head_dim:
+        raise ValueError(f"rows of {k.shape[-1]} channels, a cache of {cache.head_dim}")
+    n, dev = k.shape[0], k.device
+    kr, vr = _rows(k, "k"), _rows(v, "v")
+    sq, at = _dense(seq, "seq", "int32", (n,), dev), _dense(pos, "pos", "int32", (n,), dev)
+    n_seqs, stride = page_table.shape
+    pt = _dense(page_table, "page_table", "int32", (n_seqs, stride), dev)
+    w, table = _weight(k_weight, k, "k_weight"), _rotary_ref(rotary, dev)
+    fn = load_library().fathom_append_kv
+    _run_on(dev, stream, "fathom_append_kv",
+            lambda s: fn(ctypes.byref(cache), n, ctypes.byref(kr), ctypes.byref(vr), sq, at, pt,
+                         n_seqs, stride, table, w, eps, s))
+
+
+def fathom_paged_attention_workspace_bytes(cache: fathom_kv_cache, n_seqs: int, group: int,
+                                           max_len: int, prefix_len: int = 0) -> int:
+    return int(load_library().fathom_paged_attention_workspace_bytes(
+        ctypes.byref(cache), int(n_seqs), int(group), int(max_len), int(prefix_len)))
+
+
+def _attention_args(cache, q, page_table, seq_lens, out, workspace, slopes):
+    _same_shape(q, out, "out")
+    if q.shape[-1] != cache.head_dim:
+        raise ValueError(f"rows of {q.shape[-1]} channels, a cache of {cache.head_dim}")
+    dev, n = q.device, q.shape[0]
+    stride = page_table.shape[-1]
+    if workspace is not None and workspace.device != dev:
+        raise ValueError(f"workspace on {workspace.device}, rows on {dev}")
+    return (ctypes.byref(_rows(q, "q")), _dense(page_table, "page_table", "int32", (n, stride), dev),
+            stride, _dense(seq_lens, "seq_lens", "int32", (n,), dev), n,
+            0 if slopes is None else _dense(slopes, "slopes", "float32", q.shape[1:2], dev),
+            ctypes.byref(_rows(out, "out")), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def fathom_paged_attention(cache: fathom_kv_cache, q, page_table, seq_lens, max_len: int, out,
+                           workspace, softmax_scale: float, prefix_len: int = 0,
+                           softcap: float = 0.0, slopes=None, stream=None):
+    """Attention of one query token per sequence, q [n_seqs][Hq][d], over all
+    seq_lens[b] <= max_len keys of its pages; the first prefix_len keys are the
+    same pages in every row of page_table."""
+    rows, pt, stride, sl, n, sp, out_rows, ws, nbytes = _attention_args(
+        cache, q, page_table, seq_lens, out, workspace, slopes)
+    fn = load_library().fathom_paged_attention
+    _run_on(q.device, stream, "fathom_paged_attention",
+            lambda s: fn(ctypes.byref(cache), rows, pt, stride, sl, n, max_len, prefix_len,
+                         softmax_scale, softcap, sp, out_rows, ws, nbytes, s))
+
+
+def fathom_sparse_attention_paged_workspace_bytes(n_seqs: int, n_heads: int, head_dim: int,
+                                                  k: int) -> int:
+    return int(load_library().fathom_sparse_attention_paged_workspace_bytes(
+        int(n_seqs), int(n_heads), int(head_dim), int(k)))
+
+
+def fathom_sparse_attention_paged(cache: fathom_kv_cache, q, idx, page_table, seq_lens, out,
+                                  workspace, softmax_scale: float, softcap: float = 0.0,
+                                  slopes=None, stream=None):
+    """Attention of each query head of q [n_seqs][Hq][d] over the keys that
+    idx (int32 [n_seqs][Hq][k], -1: no key) lists of its sequence's pages."""
+    rows, pt, stride, sl, n, sp, out_rows, ws, nbytes = _attention_args(
+        cache, q, page_table, seq_lens, out, workspace, slopes)
+    k = idx.shape[-1]
+    ix = _dense(idx, "idx", "int32", (n, q.shape[1], k), q.device)
+    fn = load_library().fathom_sparse_attention_paged
+    _run_on(q.device, stream, "fathom_sparse_attention_paged",
+            lambda s: fn(ctypes.byref(cache), rows, ix, k, pt, stride, sl, n, softmax_scale,
+                         softcap, sp, out_rows, ws, nbytes, s))
+
+
 def fathom_last_device_status(stream=None) -> int:
     return int(load_library().fathom_last_device_status(_stream(stream)))
 
@@ -397,3 +631,80 @@ def plan_and_scan(index: KeyIndex, q_bf16, budget, buf: ScanBuffers, flags: int 
     fathom_scan_topk(index.desc, q_bf16, buf.t, buf.t_union, buf.k, buf.idx, buf.score,
                      buf.workspace, flags, stream)
     return buf
+
+
+class RotaryTable:
+    """Owns the device table of a position rotation and its C descriptor.
+
+    rotary_dim: channels of a head that are rotated (default: all of
+    head_dim).  interleaved: pairs are (2i, 2i + 1) instead of (i, i +
+    rotary_dim/2).  scaling: "none", "linear", "ntk" or "yarn", stretched by
+    factor (fathom_rotary_turns gives the formulas)."""
+
+    _SCALINGS = {"none": FATHOM_ROTARY_PLAIN, "linear": FATHOM_ROTARY_LINEAR,
+                 "ntk": FATHOM_ROTARY_NTK, "yarn": FATHOM_ROTARY_YARN}
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, base: float = 10000.0,
+                 interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                 original_len: int = 1, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 device: Optional[int] = None):
+        import torch
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if rotary_dim > head_dim:
+            raise ValueError(f"rotary_dim {rotary_dim} of a head of {head_dim} channels")
+        if scaling not in self._SCALINGS:
+            raise ValueError(f"scaling is one of {', '.join(self._SCALINGS)}, not {scaling!r}")
+        turns, magnitude = fathom_rotary_turns(rotary_dim, base, self._SCALINGS[scaling], factor,
+                                               original_len, beta_fast, beta_slow)
+        self.device = torch.device("cuda", torch.cuda.current_device() if device is None
+                                   else device)
+        self.turns = torch.tensor(turns, dtype=torch.float64, device=self.device)
+        self.magnitude = magnitude
+        self.desc = fathom_rotary(self.turns.data_ptr(), rotary_dim, int(interleaved), magnitude)
+
+
+class PagedKV:
+    """Owns (or refers to) the tensors of a paged K/V cache and its C
+    descriptor.  k and v are [n_pages][H][page_size][d]; order "token_major"
+    stores them as [n_pages][page_size][H][d] instead (the views keep the
+    first order).  residency "host_mapped" keeps the pages in pinned host
+    memory, for fathom_append_kv and fathom_sparse_attention_paged."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int = 128,
+                 dtype=None, order: str = "head_major", residency: str = "device",
+                 device: Optional[int] = None):
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if order not in ("head_major", "token_major"):
+            raise ValueError(f"unknown order {order!r}")
+        if residency not in ("device", "host_mapped"):
+            raise ValueError(f"unknown residency {residency!r}")
+        dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        shape = [n_pages, n_kv_heads, page_size, head_dim]
+        if order == "token_major":
+            shape[1], shape[2] = shape[2], shape[1]
+        where = dict(device=dev) if residency == "device" else dict(pin_memory=True)
+        k, v = (torch.zeros(shape, dtype=dtype, **where) for _ in range(2))
+        if order == "token_major":
+            k, v = k.transpose(1, 2), v.transpose(1, 2)
+        self._set(k, v)
+
+    @classmethod
+    def from_tensors(cls, k, v):
+        """A cache over existing tensors [n_pages][H][page_size][d] (views of
+        any order of the first three axes, channels contiguous, equal strides)."""
+        self = cls.__new__(cls)
+        self._set(k, v)
+        return self
+
+    def _set(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype \
+                or k.device != v.device or k.stride(3) != 1:
+            raise ValueError("k and v: [n_pages][H][page_size][d] of one type, device and layout, "
+                             "channels contiguous")
+        if not (k.is_cuda or (k.is_pinned() and v.is_pinned())):
+            raise ValueError("k and v: device or pinned host memory")
+        self.k, self.v = k, v
+        self.desc = fathom_kv_cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                                    k.stride(2), k.shape[0], k.shape[2], k.shape[1], k.shape[3],
+                                    _dtype_code(k.dtype))

@@ -119,6 +119,84 @@ cudaError_t launch_merge(const int32_t *idx, const float *score, const MergeOffs
                          int Q, int k_s, int k, int32_t *out_idx, float *out_score,
                          cudaStream_t stream);
 
+// ---- rotary.cu
+// One kind of head rows (queries, keys or values) on its way through
+// launch_rows: input view, output view (out_ts unused when paged), norm weight
+// or null, and whether its pairs are rotated.
+struct RowSet {
+    const void *in;
+    void *out;
+    const void *weight;
+    long long in_ts, in_hs, out_ts, out_hs;
+    int heads;
+    int out_dtype;
+    int turn;
+};
+struct RowsArgs {
+    RowSet set[2];               // heads 0 where there is none
+    const int32_t *pos;          // [n_tokens]
+    const double *turns;         // [rotary_dim / 2]
+    float magnitude, eps;
+    int n_tokens, head_dim;
+    int rotary_dim, interleaved; // rotary_dim 0: no rotation
+    // rows that go to the pages of a cache: out is its k or v, out_hs its
+    // head stride
+    int paged;
+    const int32_t *seq, *table;
+    int n_seqs, table_stride, n_pages, page_shift;
+    long long page_stride, slot_stride;
+    // set by the launcher
+    int lanes, tile, heads_per_cta;
+    int *status;
+};
+// dtype: type of every input row and weight.  vector: all bases and strides
+// allow 16-byte accesses of 8 elements and rotary_dim is a multiple of 16.
+cudaError_t launch_rows(RowsArgs a, int dtype, bool vector, cudaStream_t stream);
+
+// ---- paged_attention.cu, paged_sparse.cu
+struct PagedView {               // a paged cache and its table, device addresses
+    const void *k, *v;
+    long long page_stride, head_stride, slot_stride;
+    int n_pages, page_shift, n_kv_heads, head_dim, dtype;
+    const int32_t *table;
+    int table_stride;
+};
+struct PagedQuery {              // the query rows, the scores and the output rows
+    const void *q;
+    void *out;
+    long long q_ts, q_hs, out_ts, out_hs;
+    const int32_t *seq_lens;
+    const float *slopes;
+    float softmax_scale, softcap;
+    int n_seqs, group;
+};
+size_t paged_attention_bytes(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len,
+                             int prefix_len);
+cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int max_len,
+                                   int prefix_len, void *ws, cudaStream_t stream);
+size_t paged_sparse_bytes(int n_rows, int head_dim, int k);
+cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const int32_t *idx, int k,
+                                void *ws, cudaStream_t stream);
+
+// ---- paged_merge.cu
+// Parts of an attention row that were computed apart: part p of row r has the
+// sum sum_j 2^(s_j - max) V_j [d] at o + (r*parts + p)*d and (max, sum_j
+// 2^(s_j - max)) at ml + (r*parts + p)*2, s in powers of two.
+struct PartsView {
+    float *o;
+    float2 *ml;
+    int parts;                   // places per row
+};
+size_t parts_bytes(int rows, int head_dim, int parts);
+PartsView parts_carve(void *ws, int rows, int head_dim, int parts);
+// out[row] = sum of the row's parts over the sum of their weights, zeros where
+// that is 0.  Of a row's places the first `fixed` and then one per `chunk`
+// keys past `first` of its sequence are written (chunk 0: all of them); a
+// sequence of length 0, or refused (outside [shared, max_len]), has none.
+cudaError_t launch_merge_parts(const PartsView &pv, const PagedQuery &q, int n_heads, int head_dim,
+                               int dtype, int fixed, int shared, int first, int chunk,
+                               int max_len, cudaStream_t stream);
+
 // ---- scan.cu
 struct ScanSessionArgs {
     const fathom_index *ix;

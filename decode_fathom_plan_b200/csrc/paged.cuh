@@ -1,0 +1,79 @@
+// Shared by the kernels of the paged cache: element types, addresses of
+// cached rows, and the scores of the attention kernels (internal).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace fathom {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------ element types
+template <typename T>
+__device__ __forceinline__ float2 widen2(uint32_t u);
+template <>
+__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t u)
+{
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 widen2<__half>(uint32_t u)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+// Two floats rounded to nearest even, a in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t narrow2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow2<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// -------------------------------------------------------------------- scores
+// 2^x, within 2^-22 of the value; 2^-inf = 0.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A dot product as a logit times log2(e), so that the softmax is a power of
+// two.  The cap is cap * tanh(x / cap) with tanh(y) = 1 - 2 / (1 + e^2y): its
+// error is some 2^-23 of the cap, an absolute one of a logit; the hardware's
+// own tanh is 2^-11 off, 0.02 of a logit at a cap of 50.
+struct ScoreArgs {
+    float scale;      // softmax_scale * log2(e); with a cap 2 * log2(e) * softmax_scale / cap
+    float cap;        // cap * log2(e), or 0 without a cap
+};
+__device__ __forceinline__ float score_logit(float dot, const ScoreArgs &s)
+{
+    const float x = dot * s.scale;
+    if (s.cap == 0.0f) return x;
+    return s.cap * (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x)));
+}
+
+inline ScoreArgs score_args(float softmax_scale, float softcap)
+{
+    return softcap > 0.0f ? ScoreArgs{2.0f * kLog2e * softmax_scale / softcap, softcap * kLog2e}
+                          : ScoreArgs{kLog2e * softmax_scale, 0.0f};
+}
+
+// Scores may pass the reference maximum by this many powers of two before
+// the sums are rescaled to a new one: 2^8 more in a float32 sum costs no
+// accuracy, fits float16, and most tiles then rescale nothing.
+constexpr float kRescale = 8.0f;
+
+}  // namespace fathom

@@ -1,0 +1,234 @@
+// Attention of each query head over the keys its top-k selected, gathered from
+// a paged cache: the paged, batched form of the attention after the scan
+// (Fathom explainer, papers.ananclaw.com, arXiv 2609.17652, section
+// 解决什么真问题: the decode step attends over the selected rows of the cache).
+//
+// Every list is its query's own, so a key row serves one query: 4*d flops for
+// 4*d bytes of K and V, and only the reads count.  Four lanes share a key,
+// lane t holding channels [32j + 8t, +8), so a 16-byte load of each brings 64
+// bytes of the row, a warp has eight keys at once, a dot product costs two
+// shuffles, and the sums over V need none: each group of four lanes keeps its
+// own running maximum, sum and output, which are joined once at the end.
+// A query's list is split into runs of kRunKeys keys, one CTA each.
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace fathom {
+namespace {
+
+constexpr int kSparseThreads = 128;
+constexpr int kSparseWarps = kSparseThreads / 32;
+constexpr int kRunKeys = 128;
+
+struct SparseArgs {
+    PagedView kv;
+    PagedQuery q;
+    PartsView pv;
+    ScoreArgs score;
+    const int32_t *idx;
+    int k, direct;
+    int *status;
+};
+
+// grid (runs, query heads, sequences)
+template <typename T, int E>
+__global__ void __launch_bounds__(kSparseThreads)
+paged_sparse_kernel(const SparseArgs a)
+{
+    constexpr int d = 32 * E;
+    __shared__ float s_m[kSparseWarps], s_l[kSparseWarps];
+    __shared__ alignas(16) float s_o[kSparseWarps][d];
+    const int b = blockIdx.z, head = blockIdx.y, run = blockIdx.x, n_heads = gridDim.y;
+    const int h = head / a.q.group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int n = a.q.seq_lens[b];
+    const int32_t *table = a.kv.table + (size_t)b * a.kv.table_stride;
+    const int32_t *idx = a.idx + ((size_t)b * n_heads + head) * a.k;
+    const int shift = a.kv.page_shift, mask = (1 << shift) - 1;
+    const T *K = static_cast<const T *>(a.kv.k) + h * a.kv.head_stride + 8 * t;
+    const T *V = static_cast<const T *>(a.kv.v) + h * a.kv.head_stride + 8 * t;
+    const float slope = a.q.slopes ? a.q.slopes[head] * kLog2e : 0.0f;
+
+    uint4 qr[E];
+    {
+        const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + head * a.q.q_hs + 8 * t;
+#pragma unroll
+        for (int j = 0; j < E; ++j) qr[j] = *reinterpret_cast<const uint4 *>(q + 32 * j);
+    }
+    float m = -INFINITY, l = 0.0f, o[E][8];
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[j][x] = 0.0f;
+    bool bad = false;
+
+    const int i1 = min(a.k, (run + 1) * kRunKeys);
+    for (int i0 = run * kRunKeys + warp * 8; i0 < i1; i0 += kSparseWarps * 8) {
+        const int i = i0 + (lane >> 2);
+        const int key = i < i1 ? idx[i] : -1;
+        long long at = -1;
+        if (key != -1) {
+            int page = -1;
+            if (key >= 0 && key < n && (key >> shift) < a.kv.table_stride) page = table[key >> shift];
+            if (page >= 0 && page < a.kv.n_pages)
+                at = page * a.kv.page_stride + (key & mask) * a.kv.slot_stride;
+            else
+                bad = true;
+        }
+        uint4 kr[E], vr[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            kr[j] = vr[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (at >= 0) {
+                kr[j] = __ldg(reinterpret_cast<const uint4 *>(K + at + 32 * j));
+                vr[j] = __ldg(reinterpret_cast<const uint4 *>(V + at + 32 * j));
+            }
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const uint32_t ku[4] = {kr[j].x, kr[j].y, kr[j].z, kr[j].w};
+            const uint32_t qu[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 kf = widen2<T>(ku[x]), qf = widen2<T>(qu[x]);
+                dot = fmaf(kf.x, qf.x, fmaf(kf.y, qf.y, dot));
+            }
+        }
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
+        const float s = at >= 0 ? score_logit(dot, a.score) - slope * (float)(n - 1 - key) : -INFINITY;
+        if (__any_sync(0xFFFFFFFFu, s > m + kRescale)) {
+            const float next = fmaxf(m, s);
+            const float w = m == next ? 1.0f : exp2_fast(m - next);
+            m = next;
+            l *= w;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) o[j][x] *= w;
+        }
+        const float p = exp2_fast(s - (m == -INFINITY ? 0.0f : m));
+        l += p;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const uint32_t vu[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 vf = widen2<T>(vu[x]);
+                o[j][2 * x] = fmaf(p, vf.x, o[j][2 * x]);
+                o[j][2 * x + 1] = fmaf(p, vf.y, o[j][2 * x + 1]);
+            }
+        }
+    }
+    if (bad) set_status(a.status, FATHOM_ERR_INVALID_ARG);
+
+    // join the warp's eight key groups, then the warps
+    float top = m;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    const float w = top == -INFINITY ? 0.0f : exp2_fast(m - top);
+    l *= w;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            o[j][x] *= w;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) o[j][x] += __shfl_xor_sync(0xFFFFFFFFu, o[j][x], off);
+        }
+    if (lane < 4) {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+#pragma unroll
+            for (int x = 0; x < 8; x += 4)
+                *reinterpret_cast<float4 *>(&s_o[warp][32 * j + 8 * t + x]) =
+                    make_float4(o[j][x], o[j][x + 1], o[j][x + 2], o[j][x + 3]);
+        if (lane == 0) {
+            s_m[warp] = top;
+            s_l[warp] = l;
+        }
+    }
+    __syncthreads();
+    const int c0 = threadIdx.x * 4;
+    if (c0 >= d) return;
+    top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kSparseWarps; ++x) top = fmaxf(top, s_m[x]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kSparseWarps; ++x) {
+        const float f = exp2_fast(s_m[x] - ref);
+        const float4 v = *reinterpret_cast<const float4 *>(&s_o[x][c0]);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+        sum += f * s_l[x];
+    }
+    if (a.direct) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t *out = static_cast<uint16_t *>(a.q.out) + b * a.q.out_ts + head * a.q.out_hs + c0;
+        *reinterpret_cast<uint2 *>(out) = make_uint2(narrow2<T>(acc.x * inv, acc.y * inv),
+                                                     narrow2<T>(acc.z * inv, acc.w * inv));
+    } else {
+        const size_t place = ((size_t)b * n_heads + head) * a.pv.parts + run;
+        *reinterpret_cast<float4 *>(a.pv.o + place * d + c0) = acc;
+        if (c0 == 0) a.pv.ml[place] = make_float2(top, sum);
+    }
+}
+
+template <typename T>
+void launch_sparse(const SparseArgs &a, dim3 grid, cudaStream_t stream)
+{
+    switch (a.kv.head_dim / 32) {
+    case 1: paged_sparse_kernel<T, 1><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 2: paged_sparse_kernel<T, 2><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 3: paged_sparse_kernel<T, 3><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 4: paged_sparse_kernel<T, 4><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 5: paged_sparse_kernel<T, 5><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 6: paged_sparse_kernel<T, 6><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 7: paged_sparse_kernel<T, 7><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    default: paged_sparse_kernel<T, 8><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    }
+}
+
+int sparse_runs(int k) { return (k - 1) / kRunKeys + 1; }
+
+}  // namespace
+
+size_t paged_sparse_bytes(int n_rows, int head_dim, int k)
+{
+    return sparse_runs(k) == 1 ? 0 : parts_bytes(n_rows, head_dim, sparse_runs(k));
+}
+
+cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const int32_t *idx, int k,
+                                void *ws, cudaStream_t stream)
+{
+    const int n_heads = kv.n_kv_heads * q.group, runs = sparse_runs(k);
+    SparseArgs a{};
+    a.kv = kv;
+    a.q = q;
+    a.score = score_args(q.softmax_scale, q.softcap);
+    a.idx = idx;
+    a.k = k;
+    a.direct = runs == 1;
+    if (!a.direct) a.pv = parts_carve(ws, q.n_seqs * n_heads, kv.head_dim, runs);
+    a.status = device_status_ptr();
+    const dim3 grid(runs, n_heads, q.n_seqs);
+    if (kv.dtype == FATHOM_BF16)
+        launch_sparse<__nv_bfloat16>(a, grid, stream);
+    else
+        launch_sparse<__half>(a, grid, stream);
+    note_launch();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.direct) return e;
+    return launch_merge_parts(a.pv, q, n_heads, kv.head_dim, kv.dtype, 0, 0, 0, 0, 0, stream);
+}
+
+}  // namespace fathom

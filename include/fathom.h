@@ -379,6 +379,195 @@ fathom_status fathom_sparse_attention(const float *keys, const float *values, in
                                       size_t workspace_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------- */
+/* The step around the scan on a paged 16-bit K/V cache.                  */
+/* ---------------------------------------------------------------------- */
+
+/* A serving stack hands a decode step the raw query, key and value rows of
+ * its projection and keeps K and V in pages that its sequences own or share.
+ * The calls below take those as they are: fathom_qk_norm_rope turns raw
+ * query and key rows into the q that fathom_plan takes (and the float32 keys
+ * that fathom_pack_keys and fathom_append_keys take), fathom_append_kv writes
+ * keys and values into the pages, fathom_sparse_attention_paged attends over
+ * the keys that fathom_scan_topk selected, and fathom_paged_attention over
+ * every key of a sequence.  All are stream-ordered, may be captured in a
+ * CUDA graph, allocate nothing and make no host synchronisation. */
+
+/* Element types of rows and caches. */
+typedef enum {
+    FATHOM_F32 = 0,
+    FATHOM_BF16 = 1,
+    FATHOM_F16 = 2
+} fathom_dtype;
+
+/* A view of head rows: channel c of head h of token t is element
+ * t*token_stride + h*head_stride + c of data (strides in elements, 64-bit
+ * arithmetic; the d channels of a row are contiguous).  data: a device
+ * pointer.  Rows of a packed projection [T][Hq + 2*Hkv][d], token-major and
+ * head-major tensors are all such views. */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t n_heads;
+    int32_t dtype;            /* fathom_dtype */
+} fathom_rows;
+
+/* Position rotation of the first rotary_dim channels of a head: pair i of
+ * position p is turned by the angle 2*pi * p * turns[i] and scaled by
+ * magnitude.  Pairs are channels (i, i + rotary_dim/2), or (2i, 2i + 1) when
+ * interleaved is non-zero; channels from rotary_dim on are passed through.
+ * turns: device float64 [rotary_dim/2], e.g. from fathom_rotary_turns. */
+typedef struct {
+    const double *turns;
+    int32_t rotary_dim;       /* even, 2..head_dim */
+    int32_t interleaved;      /* 0 or 1 */
+    float magnitude;
+} fathom_rotary;
+
+/* Frequency scalings of fathom_rotary_turns. */
+typedef enum {
+    FATHOM_ROTARY_PLAIN = 0,
+    FATHOM_ROTARY_LINEAR = 1,
+    FATHOM_ROTARY_NTK = 2,
+    FATHOM_ROTARY_YARN = 3
+} fathom_rotary_scaling;
+
+/* Host helper: fill the host array turns [rotary_dim/2] and *magnitude.
+ * With f_i = base^(-2i/rotary_dim) radians per position, turns_i is
+ *   PLAIN   f_i / 2pi                                        (factor unused)
+ *   LINEAR  f_i / (2pi*factor)               (position interpolation)
+ *   NTK     f_i / 2pi with base * factor^(rotary_dim/(rotary_dim-2))
+ *   YARN    f_i * (g + (1-g)/factor) / 2pi, where a pair that turns
+ *           r = original_len * f_i / 2pi times over the original context has
+ *           g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1)
+ *           (Peng et al., "YaRN", 2023, the by-parts interpolation)
+ * and magnitude 1, or 0.1*ln(factor) + 1 for YARN.
+ * rotary_dim even and >= 2 (>= 4 for NTK), base > 0, factor >= 1 where it is
+ * used, beta_fast > beta_slow and original_len >= 1 for YARN. */
+fathom_status fathom_rotary_turns(double *turns, float *magnitude, int32_t rotary_dim, double base,
+                                  int32_t scaling, double factor, int64_t original_len,
+                                  double beta_fast, double beta_slow);
+
+/* Norm and rotation of query and key heads in one pass.  For each row x of q
+ * and k (d = head_dim channels),
+ *   y = x * w / sqrt(mean(x^2) + eps)   (w = q_weight or k_weight; y = x
+ *                                        where that weight is NULL),
+ * then y's pairs are rotated to position pos[t] (left as they are where
+ * rotary is NULL) and written to the out rows in their type.  Norm and
+ * products in float32; an angle is reduced to a fraction of a turn in
+ * float64, so that far positions keep full accuracy; one rounding at the end.
+ * q and q_out, k and k_out: rows of n_tokens tokens with the same number of
+ * heads; either pair may be NULL, not both.  q and k have one type, the outs
+ * any (e.g. bf16 q for fathom_plan, float32 head-major k for
+ * fathom_pack_keys).  An out may be its input itself (same data, strides and
+ * type), and overlaps nothing otherwise.  weights: device [d] in the type of
+ * q and k.  pos: device int32 [n_tokens], NULL only where rotary is.
+ * n_tokens may be 0.  head_dim a multiple of 32, at most 256. */
+fathom_status fathom_qk_norm_rope(int32_t n_tokens, int32_t head_dim, const int32_t *pos,
+                                  const fathom_rotary *rotary, const void *q_weight,
+                                  const void *k_weight, float eps, const fathom_rows *q,
+                                  const fathom_rows *q_out, const fathom_rows *k,
+                                  const fathom_rows *k_out, cudaStream_t stream);
+
+/* A paged K/V cache: channel c of KV head h of the key in slot s of page p is
+ * element p*page_stride + h*head_stride + s*token_stride + c of k (of v for
+ * its value); strides in elements.  k and v: device memory, or pinned host
+ * memory used through its device mapping (an offloaded cache; not for
+ * fathom_paged_attention); 16-byte aligned, strides multiples of 8.
+ * A page table is device int32 [n_seqs][table_stride]: key j of sequence b
+ * lies in slot j % page_size of page page_table[b][j / page_size].
+ * Sequences may share pages.  Entries behind a sequence's last key are never
+ * read.  A page index outside [0, n_pages) is never dereferenced and sets
+ * FATHOM_ERR_INVALID_ARG in the device status (what it was to hold is
+ * skipped). */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t token_stride;
+    int32_t n_pages;
+    int32_t page_size;        /* a power of two, 8..1024 */
+    int32_t n_kv_heads;
+    int32_t head_dim;         /* a multiple of 32, at most 256 */
+    int32_t dtype;            /* FATHOM_BF16 or FATHOM_F16 */
+} fathom_kv_cache;
+
+/* Write new keys and values into a paged cache, each key normed (k_weight)
+ * and rotated to its position (rotary) on the way, as fathom_qk_norm_rope
+ * does; values are only converted.  Token t goes to position pos[t] of
+ * sequence seq[t]: the slot of the page that the sequence's table names, and
+ * the position that its key is rotated to.  seq[t] < 0 marks a padding token,
+ * which is skipped.  A sequence >= n_seqs, a position outside
+ * [0, table_stride*page_size) or a bad page skips the token and sets
+ * FATHOM_ERR_INVALID_ARG in the device status.  Two tokens of one call must
+ * not have the same slot (its contents are then those of either, channel by
+ * channel).  Nothing else in the cache is written.
+ * k, v: rows of n_tokens tokens with the cache's heads, one type.  seq, pos:
+ * device int32 [n_tokens].  n_tokens may be 0. */
+fathom_status fathom_append_kv(const fathom_kv_cache *cache, int32_t n_tokens, const fathom_rows *k,
+                               const fathom_rows *v, const int32_t *seq, const int32_t *pos,
+                               const int32_t *page_table, int32_t n_seqs, int32_t table_stride,
+                               const fathom_rotary *rotary, const void *k_weight, float eps,
+                               cudaStream_t stream);
+
+/* Workspace bytes fathom_paged_attention needs (0 for invalid sizes). */
+size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int32_t n_seqs,
+                                              int32_t group, int32_t max_len, int32_t prefix_len);
+
+/* Softmax attention of one query token per sequence over all its keys.  For
+ * query head i = h*G + g of sequence b with n = seq_lens[b] keys,
+ *   s_j = softmax_scale * (q[b][i] . K_j),
+ *   s_j = softcap * tanh(s_j / softcap)     where softcap > 0,
+ *   s_j = s_j - slopes[i] * (n - 1 - j)     where slopes is not NULL
+ *                                           (the query stands at n - 1),
+ *   out[b][i] = sum_j softmax(s)_j V_j,  j in [0, n).
+ * A sequence of length 0 (a padded batch row) gets zeros.
+ * prefix_len > 0 states that the first prefix_len keys (a multiple of
+ * page_size) are the same pages in every row of the table: they are read from
+ * the first row and multiplied with the queries of all sequences at once.
+ * Every length is then 0 or at least prefix_len.  seq_lens (device int32
+ * [n_seqs]) may change between replays of a captured call; max_len is the
+ * host's bound on them.  A length that is negative, above max_len or, if not
+ * 0, below prefix_len sets FATHOM_ERR_INVALID_ARG in the device status, and
+ * that sequence gets zeros.  A key on a bad page is skipped (one of the
+ * prefix takes part with a K and V of zeros).
+ * q, out: rows of n_seqs tokens with G*n_kv_heads heads, in the cache's type,
+ * 16-byte aligned, strides multiples of 8; G 1..8.  slopes: device float32
+ * [G*n_kv_heads].  Scores, softmax and sums are float32; each probability is
+ * rounded to the cache's type for its product with V, which is accumulated in
+ * float32.  workspace: device memory that no other call in flight uses. */
+fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_rows *q,
+                                     const int32_t *page_table, int32_t table_stride,
+                                     const int32_t *seq_lens, int32_t n_seqs, int32_t max_len,
+                                     int32_t prefix_len, float softmax_scale, float softcap,
+                                     const float *slopes, const fathom_rows *out, void *workspace,
+                                     size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes fathom_sparse_attention_paged needs (0 for invalid sizes). */
+size_t fathom_sparse_attention_paged_workspace_bytes(int32_t n_seqs, int32_t n_heads,
+                                                     int32_t head_dim, int32_t k);
+
+/* fathom_sparse_attention on a paged cache, for a batch of sequences: query
+ * head i of sequence b attends over the keys idx[b][i][0..k) of its sequence
+ * (e.g. fathom_scan_topk's out_idx), with the scores of
+ * fathom_paged_attention.  idx: device int32 [n_seqs][G*n_kv_heads][k]; an
+ * entry of -1 is no key (lists of sequences with fewer keys are padded with
+ * it); a list of nothing else gives zeros.  A key listed twice counts twice.
+ * An entry below -1 or >= seq_lens[b], or one on a bad page, is skipped and
+ * sets FATHOM_ERR_INVALID_ARG in the device status.  k and v of the cache may
+ * be pinned host memory: only the listed rows cross the link.  q, out, slopes
+ * and workspace as for fathom_paged_attention; all arithmetic is float32,
+ * with one rounding of the output. */
+fathom_status fathom_sparse_attention_paged(const fathom_kv_cache *cache, const fathom_rows *q,
+                                            const int32_t *idx, int32_t k,
+                                            const int32_t *page_table, int32_t table_stride,
+                                            const int32_t *seq_lens, int32_t n_seqs,
+                                            float softmax_scale, float softcap, const float *slopes,
+                                            const fathom_rows *out, void *workspace,
+                                            size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* Status and instrumentation.                                            */
 /* ---------------------------------------------------------------------- */
 
