@@ -197,6 +197,17 @@ cudaError_t launch_merge_parts(const PartsView &pv, const PagedQuery &q, int n_h
                                int dtype, int fixed, int shared, int first, int chunk,
                                int max_len, cudaStream_t stream);
 
+// ---- paged_prefix.cu
+// How the products over a shared prefix are split: rows of a KV head, CTAs of
+// up to two blocks of 128 of them, runs of key tiles, places per row.
+struct PrefixPlan {
+    int rows, two_blocks, row_groups, n_tiles, splits, parts;
+};
+PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int prefix_len);
+// Writes the first p.parts places of every row.
+cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const PrefixPlan &p,
+                                const PartsView &pv, int prefix_len, cudaStream_t stream);
+
 // ---- scan.cu
 struct ScanSessionArgs {
     const fathom_index *ix;

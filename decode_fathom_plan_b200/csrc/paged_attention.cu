@@ -311,17 +311,19 @@ int chunk_keys(int n_kv_heads, int n_seqs, int own)
 }
 
 struct Plan {
-    int chunk, chunks, fixed, parts, direct;
+    PrefixPlan prefix;
+    int first, chunk, chunks, parts, direct;
 };
-Plan plan_parts(int n_kv_heads, int n_seqs, int max_len, int prefix_len)
+Plan plan_parts(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len, int prefix_len)
 {
     Plan p{};
-    const int own = max_len - prefix_len;
+    p.prefix = plan_prefix(n_kv_heads, head_dim, n_seqs, group, prefix_len);
+    p.first = p.prefix.parts ? prefix_len : 0;
+    const int own = max_len - p.first;
     p.chunk = chunk_keys(n_kv_heads, n_seqs, own);
-    p.chunks = std::max(1, (own + p.chunk - 1) / p.chunk);
-    p.fixed = 0;
-    p.parts = p.fixed + p.chunks;
-    p.direct = p.parts == 1;
+    p.chunks = (own + p.chunk - 1) / p.chunk;
+    p.parts = p.prefix.parts + p.chunks;
+    p.direct = p.parts == 1 && p.chunks == 1;
     return p;
 }
 
@@ -330,14 +332,14 @@ Plan plan_parts(int n_kv_heads, int n_seqs, int max_len, int prefix_len)
 size_t paged_attention_bytes(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len,
                              int prefix_len)
 {
-    const Plan p = plan_parts(n_kv_heads, n_seqs, max_len, 0 * prefix_len);
+    const Plan p = plan_parts(n_kv_heads, head_dim, n_seqs, group, max_len, prefix_len);
     return p.direct ? 0 : parts_bytes(n_seqs * n_kv_heads * group, head_dim, p.parts);
 }
 
 cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int max_len,
                                    int prefix_len, void *ws, cudaStream_t stream)
 {
-    const Plan p = plan_parts(kv.n_kv_heads, q.n_seqs, max_len, 0 * prefix_len);
+    const Plan p = plan_parts(kv.n_kv_heads, kv.head_dim, q.n_seqs, q.group, max_len, prefix_len);
     const int n_heads = kv.n_kv_heads * q.group;
     SplitArgs a{};
     a.kv = kv;
@@ -345,21 +347,27 @@ cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int
     if (!p.direct) a.pv = parts_carve(ws, q.n_seqs * n_heads, kv.head_dim, p.parts);
     a.score = score_args(q.softmax_scale, q.softcap);
     a.shared = prefix_len;
-    a.first = 0;
-    a.fixed = p.fixed;
+    a.first = p.first;
+    a.fixed = p.prefix.parts;
     a.chunk = p.chunk;
     a.max_len = max_len;
     a.direct = p.direct;
     a.status = device_status_ptr();
-    const dim3 grid(p.chunks, kv.n_kv_heads, q.n_seqs);
-    if (kv.dtype == FATHOM_BF16)
-        launch_split<__nv_bfloat16>(a, grid, stream);
-    else
-        launch_split<__half>(a, grid, stream);
-    note_launch();
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.direct) return e;
-    return launch_merge_parts(a.pv, q, n_heads, kv.head_dim, kv.dtype, p.fixed, prefix_len, a.first,
+    if (p.prefix.parts) {
+        const cudaError_t e = launch_paged_prefix(kv, q, p.prefix, a.pv, prefix_len, stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.chunks) {
+        const dim3 grid(p.chunks, kv.n_kv_heads, q.n_seqs);
+        if (kv.dtype == FATHOM_BF16)
+            launch_split<__nv_bfloat16>(a, grid, stream);
+        else
+            launch_split<__half>(a, grid, stream);
+        note_launch();
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess || p.direct) return e;
+    }
+    return launch_merge_parts(a.pv, q, n_heads, kv.head_dim, kv.dtype, a.fixed, prefix_len, a.first,
                               p.chunk, max_len, stream);
 }
 

@@ -16,7 +16,7 @@ constexpr int kMergeThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads)
 merge_parts_kernel(const PartsView pv, const PagedQuery q, int n_heads, int d, int fixed, int shared,
-                   int first, int chunk, int max_len)
+                   int first, int chunk, int max_len, int *status)
 {
     __shared__ float s_m[kMergeThreads / 32];
     __shared__ float4 s_o[kMergeThreads];
@@ -25,7 +25,9 @@ merge_parts_kernel(const PartsView pv, const PagedQuery q, int n_heads, int d, i
     int parts = pv.parts;
     if (chunk) {
         const int n = q.seq_lens[b];
-        parts = (n < 1 || n < shared || n > max_len) ? 0 : fixed + (n - first + chunk - 1) / chunk;
+        const bool refused = n < 0 || n > max_len || (n > 0 && n < shared);
+        if (refused && threadIdx.x == 0) set_status(status, FATHOM_ERR_INVALID_ARG);
+        parts = (n == 0 || refused) ? 0 : fixed + (n - first + chunk - 1) / chunk;
     }
     const float2 *ml = pv.ml + (size_t)row * pv.parts;
     float m = -INFINITY;
@@ -48,6 +50,7 @@ merge_parts_kernel(const PartsView pv, const PagedQuery q, int n_heads, int d, i
 #pragma unroll 4
         for (int p = grp; p < parts; p += groups) {
             const float2 x = ml[p];
+            if (x.x == -INFINITY && x.y == 0.0f) continue;   // no key, and no sum written
             const float4 v = o[(size_t)p * lanes + lane];
             const float w = exp2_fast(x.x - ref);
             acc.x += w * v.x;
@@ -105,10 +108,10 @@ cudaError_t launch_merge_parts(const PartsView &pv, const PagedQuery &q, int n_h
     const int rows = q.n_seqs * n_heads;
     if (dtype == FATHOM_BF16)
         merge_parts_kernel<__nv_bfloat16><<<rows, kMergeThreads, 0, stream>>>(
-            pv, q, n_heads, head_dim, fixed, shared, first, chunk, max_len);
+            pv, q, n_heads, head_dim, fixed, shared, first, chunk, max_len, device_status_ptr());
     else
         merge_parts_kernel<__half><<<rows, kMergeThreads, 0, stream>>>(
-            pv, q, n_heads, head_dim, fixed, shared, first, chunk, max_len);
+            pv, q, n_heads, head_dim, fixed, shared, first, chunk, max_len, device_status_ptr());
     note_launch();
     return cudaGetLastError();
 }
