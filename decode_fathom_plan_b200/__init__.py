@@ -1,7 +1,9 @@
-"""Python binding of libfathom.so, the sm_100a Fathom read-depth key scan.
+"""Python binding of libfathom.so, the sm_100a Fathom read-depth key scan and
+the decode step around it.
 
-Argument marshalling only: every step of the path (pack, plan, scan, select)
-runs in the library's CUDA kernels.  PyTorch supplies device memory, pinned
+Argument marshalling only (ctypes; for the calls on a paged cache a small
+native module): every step of the path (pack, plan, scan, select,
+norm and rotation, append, attention) runs in the library's CUDA kernels.  PyTorch supplies device memory, pinned
 host memory and streams.  There is no CPU fallback: if the library is
 missing or no GPU is present, the calls raise.
 
@@ -307,9 +309,27 @@ def fathom_merge_topk(shard_idx, shard_score, shard_offset, k: int, out_idx, out
 
 
 # ------------------------------------------------- calls on a paged cache
-# These take tensors, whose shapes and strides they pass on.  A tensor that the
-# C call would misread (wrong type, layout or device) raises ValueError.  The
-# call runs on the tensors' device, on `stream` or that device's current one.
+# These take tensors, whose addresses, shapes and strides _binding.so passes on
+# (csrc/binding.cpp).  A tensor that the C call would misread (wrong type,
+# layout or device) raises ValueError.  A call runs on the tensors' device, on
+# `stream` (a stream, its address or None) or that device's current one.
+_native = None
+
+
+def _load_binding():
+    global _native
+    if _native is None:
+        load_library()
+        import torch  # noqa: F401  (its libraries are loaded before the module's)
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(f"{PKG}/_binding.so is missing or does not load: build it with "
+                              "`python decode_fathom_plan_b200/build.py`") from e
+        _native = _binding
+    return _native
+
+
 _DTYPES = {}
 
 
@@ -320,57 +340,8 @@ def _dtype_code(dtype) -> int:
                         torch.float16: FATHOM_F16})
     code = _DTYPES.get(dtype)
     if code is None:
-        raise ValueError(f"float32, bfloat16 or float16 rows are wanted, not {dtype}")
+        raise ValueError(f"float32, bfloat16 or float16 is wanted, not {dtype}")
     return code
-
-
-def _rows(x, what: str) -> fathom_rows:
-    """View of a CUDA tensor [tokens][heads][channels]."""
-    if x.dim() != 3 or not x.is_cuda or (x.shape[2] > 1 and x.stride(2) != 1):
-        raise ValueError(f"{what}: a CUDA tensor [tokens][heads][channels] with contiguous "
-                         "channels is wanted")
-    return fathom_rows(x.data_ptr(), x.stride(0), x.stride(1), x.shape[1], _dtype_code(x.dtype))
-
-
-def _dense(x, what: str, dtype: str, shape, device) -> int:
-    """Address of a contiguous device tensor of the given type and shape."""
-    if str(x.dtype)[6:] != dtype or tuple(x.shape) != tuple(shape) or x.device != device \
-            or not x.is_contiguous():
-        raise ValueError(f"{what}: a contiguous {dtype} tensor {tuple(shape)} on {device} is "
-                         f"wanted, not {str(x.dtype)[6:]} {tuple(x.shape)} on {x.device}")
-    return x.data_ptr()
-
-
-def _same_shape(x, y, what: str):
-    if x.shape != y.shape or x.device != y.device:
-        raise ValueError(f"{what}: {tuple(y.shape)} on {y.device} does not fit "
-                         f"{tuple(x.shape)} on {x.device}")
-
-
-def _weight(w, rows, what: str) -> int:
-    if w is None:
-        return 0
-    return _dense(w, what, str(rows.dtype)[6:], rows.shape[2:], rows.device)
-
-
-def _run_on(device, stream, what: str, call):
-    """call(stream handle) with `device` current; raises on an error status."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        rc = call(_stream(stream))
-    else:
-        with torch.cuda.device(device):
-            rc = call(_stream(stream))
-    if rc != FATHOM_OK:
-        raise FathomError(rc, what)
-
-
-def _rotary_ref(rotary, device):
-    if rotary is None:
-        return None
-    if rotary.device != device:
-        raise ValueError(f"rotary table on {rotary.device}, rows on {device}")
-    return ctypes.byref(rotary.desc)
 
 
 def fathom_rotary_turns(rotary_dim: int, base: float = 10000.0, scaling: int = FATHOM_ROTARY_PLAIN,
@@ -392,26 +363,11 @@ def fathom_qk_norm_rope(q, k, pos, q_out, k_out, rotary=None, q_weight=None, k_w
     given) of query rows q [T][Hq][d] and key rows k [T][Hk][d] at positions
     pos (int32 [T]) into q_out and k_out; q and q_out, or k and k_out, may be
     None."""
-    lead = q if q is not None else k
-    if lead is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise ValueError("q with q_out, k with k_out, or both are wanted")
-    rows = []
-    for x, out, what in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            rows += [None, None]
-            continue
-        if x.shape[0] != lead.shape[0] or x.shape[2] != lead.shape[2] or x.device != lead.device:
-            raise ValueError("q and k differ in tokens, channels or device")
-        _same_shape(x, out, what + "_out")
-        rows += [ctypes.byref(_rows(x, what)), ctypes.byref(_rows(out, what + "_out"))]
-    n = lead.shape[0]
-    at = 0 if pos is None else _dense(pos, "pos", "int32", (n,), lead.device)
-    wq = 0 if q is None else _weight(q_weight, q, "q_weight")
-    wk = 0 if k is None else _weight(k_weight, k, "k_weight")
-    table = _rotary_ref(rotary, lead.device)
-    fn = load_library().fathom_qk_norm_rope
-    _run_on(lead.device, stream, "fathom_qk_norm_rope",
-            lambda s: fn(n, lead.shape[2], at, table, wq, wk, eps, *rows, s))
+    table, where = (None, None) if rotary is None else (rotary.desc, rotary.device_index)
+    rc = (_native or _load_binding()).qk_norm_rope(q, k, pos, q_out, k_out, table, where, q_weight,
+                                                   k_weight, eps, stream)
+    if rc:
+        raise FathomError(rc, "fathom_qk_norm_rope")
 
 
 def fathom_append_kv(cache: fathom_kv_cache, k, v, seq, pos, page_table, rotary=None,
@@ -419,19 +375,11 @@ def fathom_append_kv(cache: fathom_kv_cache, k, v, seq, pos, page_table, rotary=
     """Write key rows k and value rows v [T][H][d] to positions pos (int32 [T])
     of sequences seq (int32 [T], negative: padding) of a paged cache, each key
     normed and rotated on the way; page_table int32 [n_seqs][pages]."""
-    _same_shape(k, v, "v")
-    if k.shape[-1] != cache.head_dim:
-        raise ValueError(f"rows of {k.shape[-1]} channels, a cache of {cache.head_dim}")
-    n, dev = k.shape[0], k.device
-    kr, vr = _rows(k, "k"), _rows(v, "v")
-    sq, at = _dense(seq, "seq", "int32", (n,), dev), _dense(pos, "pos", "int32", (n,), dev)
-    n_seqs, stride = page_table.shape
-    pt = _dense(page_table, "page_table", "int32", (n_seqs, stride), dev)
-    w, table = _weight(k_weight, k, "k_weight"), _rotary_ref(rotary, dev)
-    fn = load_library().fathom_append_kv
-    _run_on(dev, stream, "fathom_append_kv",
-            lambda s: fn(ctypes.byref(cache), n, ctypes.byref(kr), ctypes.byref(vr), sq, at, pt,
-                         n_seqs, stride, table, w, eps, s))
+    table, where = (None, None) if rotary is None else (rotary.desc, rotary.device_index)
+    rc = (_native or _load_binding()).append_kv(cache, k, v, seq, pos, page_table, table, where,
+                                                k_weight, eps, stream)
+    if rc:
+        raise FathomError(rc, "fathom_append_kv")
 
 
 def fathom_paged_attention_workspace_bytes(cache: fathom_kv_cache, n_seqs: int, group: int,
@@ -440,33 +388,17 @@ def fathom_paged_attention_workspace_bytes(cache: fathom_kv_cache, n_seqs: int, 
         ctypes.byref(cache), int(n_seqs), int(group), int(max_len), int(prefix_len)))
 
 
-def _attention_args(cache, q, page_table, seq_lens, out, workspace, slopes):
-    _same_shape(q, out, "out")
-    if q.shape[-1] != cache.head_dim:
-        raise ValueError(f"rows of {q.shape[-1]} channels, a cache of {cache.head_dim}")
-    dev, n = q.device, q.shape[0]
-    stride = page_table.shape[-1]
-    if workspace is not None and workspace.device != dev:
-        raise ValueError(f"workspace on {workspace.device}, rows on {dev}")
-    return (ctypes.byref(_rows(q, "q")), _dense(page_table, "page_table", "int32", (n, stride), dev),
-            stride, _dense(seq_lens, "seq_lens", "int32", (n,), dev), n,
-            0 if slopes is None else _dense(slopes, "slopes", "float32", q.shape[1:2], dev),
-            ctypes.byref(_rows(out, "out")), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
-
-
 def fathom_paged_attention(cache: fathom_kv_cache, q, page_table, seq_lens, max_len: int, out,
                            workspace, softmax_scale: float, prefix_len: int = 0,
                            softcap: float = 0.0, slopes=None, stream=None):
     """Attention of one query token per sequence, q [n_seqs][Hq][d], over all
     seq_lens[b] <= max_len keys of its pages; the first prefix_len keys are the
     same pages in every row of page_table."""
-    rows, pt, stride, sl, n, sp, out_rows, ws, nbytes = _attention_args(
-        cache, q, page_table, seq_lens, out, workspace, slopes)
-    fn = load_library().fathom_paged_attention
-    _run_on(q.device, stream, "fathom_paged_attention",
-            lambda s: fn(ctypes.byref(cache), rows, pt, stride, sl, n, max_len, prefix_len,
-                         softmax_scale, softcap, sp, out_rows, ws, nbytes, s))
+    rc = (_native or _load_binding()).paged_attention(cache, q, page_table, seq_lens, max_len, out,
+                                                      workspace, softmax_scale, prefix_len, softcap,
+                                                      slopes, stream)
+    if rc:
+        raise FathomError(rc, "fathom_paged_attention")
 
 
 def fathom_sparse_attention_paged_workspace_bytes(n_seqs: int, n_heads: int, head_dim: int,
@@ -480,14 +412,11 @@ def fathom_sparse_attention_paged(cache: fathom_kv_cache, q, idx, page_table, se
                                   slopes=None, stream=None):
     """Attention of each query head of q [n_seqs][Hq][d] over the keys that
     idx (int32 [n_seqs][Hq][k], -1: no key) lists of its sequence's pages."""
-    rows, pt, stride, sl, n, sp, out_rows, ws, nbytes = _attention_args(
-        cache, q, page_table, seq_lens, out, workspace, slopes)
-    k = idx.shape[-1]
-    ix = _dense(idx, "idx", "int32", (n, q.shape[1], k), q.device)
-    fn = load_library().fathom_sparse_attention_paged
-    _run_on(q.device, stream, "fathom_sparse_attention_paged",
-            lambda s: fn(ctypes.byref(cache), rows, ix, k, pt, stride, sl, n, softmax_scale,
-                         softcap, sp, out_rows, ws, nbytes, s))
+    rc = (_native or _load_binding()).sparse_attention_paged(cache, q, idx, page_table, seq_lens,
+                                                             out, workspace, softmax_scale, softcap,
+                                                             slopes, stream)
+    if rc:
+        raise FathomError(rc, "fathom_sparse_attention_paged")
 
 
 def fathom_last_device_status(stream=None) -> int:
@@ -660,6 +589,7 @@ class RotaryTable:
                                    else device)
         self.turns = torch.tensor(turns, dtype=torch.float64, device=self.device)
         self.magnitude = magnitude
+        self.device_index = self.device.index
         self.desc = fathom_rotary(self.turns.data_ptr(), rotary_dim, int(interleaved), magnitude)
 
 

@@ -1,8 +1,10 @@
-"""Build libfathom.so in-tree for sm_100a with nvcc.
+"""Build libfathom.so in-tree for sm_100a with nvcc, and _binding.so with g++.
 
 Each translation unit is compiled to an object under _build/ (in parallel),
-then linked into decode_fathom_plan_b200/libfathom.so.  Rebuilds only when a
-source or header is newer than the library.
+then linked into decode_fathom_plan_b200/libfathom.so.  _binding.so is the
+Python module that passes torch tensors to the library's calls on a paged
+cache (csrc/binding.cpp).  Each is rebuilt only when a source or header is
+newer than it.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfathom.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -47,7 +51,46 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(p) <= t for p in
+               [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_binding(verbose: bool = False):
+    """Compile _binding.so against torch's headers and libfathom.so (beside it)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include")] + \
+        cpp_extension.include_paths()
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
+           "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + \
+        [x for i in includes for x in ("-isystem", i)] + [BINDING_SRC, "-o", tmp, "-L" + PKG,
+         "-l:libfathom.so", "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+         "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    if verbose:
+        print(" ".join(cmd))
+    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if p.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + p.stdout.decode(errors="replace"))
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_library(force, verbose, ptxas_info)
+    if force or not binding_up_to_date():
+        build_binding(verbose)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
