@@ -2,10 +2,10 @@
 the decode step around it.
 
 Argument marshalling only (ctypes; for the calls on a paged cache a small
-native module): every step of the path (pack, plan, scan, select,
-norm and rotation, append, attention) runs in the library's CUDA kernels.  PyTorch supplies device memory, pinned
-host memory and streams.  There is no CPU fallback: if the library is
-missing or no GPU is present, the calls raise.
+native module): every step of the path (pack, plan, scan, select, norm and
+rotation, append, attention) runs in the library's CUDA kernels.  PyTorch
+supplies device memory, pinned host memory and streams.  There is no CPU
+fallback: if the library is missing or no GPU is present, the calls raise.
 
 The entry points carry the C names of include/fathom.h and take torch
 tensors (or raw addresses) where the C call takes pointers.

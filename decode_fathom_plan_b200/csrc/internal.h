@@ -131,6 +131,9 @@ struct RowSet {
     int heads;
     int out_dtype;
     int turn;
+    // set by the launcher: whether rows only move, tokens and heads of a CTA,
+    // CTAs per token tile
+    int copy, tile, heads_per_cta, chunks;
 };
 struct RowsArgs {
     RowSet set[2];               // heads 0 where there is none
@@ -146,7 +149,9 @@ struct RowsArgs {
     int n_seqs, table_stride, n_pages, page_shift;
     long long page_stride, slot_stride;
     // set by the launcher
-    int lanes, tile, heads_per_cta;
+    int lanes;                   // that hold a row
+    int blocks0;                 // CTAs of set 0
+    float inv_dim;
     int *status;
 };
 // dtype: type of every input row and weight.  vector: all bases and strides
