@@ -184,23 +184,37 @@ cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const 
                                 void *ws, cudaStream_t stream);
 
 // ---- paged_merge.cu
-// Parts of an attention row that were computed apart: part p of row r has the
-// sum sum_j 2^(s_j - max) V_j [d] at o + (r*parts + p)*d and (max, sum_j
-// 2^(s_j - max)) at ml + (r*parts + p)*2, s in powers of two.
+// Parts of attention rows that were computed apart.  The part at place p has
+// the sum sum_j 2^(s_j - max) V_j [d] at o + p*d and (max, sum_j 2^(s_j - max))
+// at ml[p], s in powers of two.
 struct PartsView {
     float *o;
     float2 *ml;
-    int parts;                   // places per row
 };
-size_t parts_bytes(int rows, int head_dim, int parts);
-PartsView parts_carve(void *ws, int rows, int head_dim, int parts);
+size_t round16(size_t b);
+size_t parts_bytes(size_t places, int head_dim);
+// Points the parts into ws (parts_bytes(...) bytes, 16-byte aligned).
+PartsView parts_carve(void *ws, size_t places, int head_dim);
+struct MergeArgs {
+    PartsView pv;
+    PagedQuery q;
+    int n_heads, head_dim;
+    int fixed;            // parts that every row has, at row*fixed
+    // Keys past the first lens_from of a sequence were split evenly over CTAs
+    // (lens_from < 0: the fixed parts are all).  info[b*H + h] is the first
+    // and the last CTA of a KV head's rows.  One CTA: the row is finished, or
+    // with fixed parts beside it one part at full_at + row.  Several: the
+    // first CTA's part at cta_at + (2*cta + 1)*G + g, the others' at
+    // cta_at + 2*cta*G + g.
+    int lens_from;
+    const int2 *info;
+    size_t full_at, cta_at;
+    int shared, max_len;  // lengths outside {0} and [shared, max_len] are refused
+    int *status;          // set by the launcher
+};
 // out[row] = sum of the row's parts over the sum of their weights, zeros where
-// that is 0.  Of a row's places the first `fixed` and then one per `chunk`
-// keys past `first` of its sequence are written (chunk 0: all of them); a
-// sequence of length 0, or refused (outside [shared, max_len]), has none.
-cudaError_t launch_merge_parts(const PartsView &pv, const PagedQuery &q, int n_heads, int head_dim,
-                               int dtype, int fixed, int shared, int first, int chunk,
-                               int max_len, cudaStream_t stream);
+// that is 0.
+cudaError_t launch_merge_parts(const MergeArgs &a, int dtype, cudaStream_t stream);
 
 // ---- paged_prefix.cu
 // How the products over a shared prefix are split: rows of a KV head, CTAs of

@@ -71,6 +71,50 @@ inline ScoreArgs score_args(float softmax_scale, float softcap)
                           : ScoreArgs{kLog2e * softmax_scale, 0.0f};
 }
 
+// ------------------------------------------------------------------- lengths
+__host__ __device__ __forceinline__ bool refused_length(int n, int shared, int max_len)
+{
+    return n < 0 || n > max_len || (n > 0 && n < shared);
+}
+
+// ------------------------------------------------------------------- outputs
+// Four channels of an output row: sum over weight, zeros where no key took
+// part.  (The key that set a part's maximum weighs at least 2^-8 in it, so the
+// weight is 0 only then; it is NaN if a score was.)
+template <typename T>
+__device__ __forceinline__ void store_row(const PagedQuery &q, int b, int head, int c, float4 sum, float weight)
+{
+    const float inv = weight == 0.0f ? 0.0f : 1.0f / weight;
+    uint16_t *out = static_cast<uint16_t *>(q.out) + b * q.out_ts + head * q.out_hs + c;
+    *reinterpret_cast<uint2 *>(out) =
+        weight == 0.0f ? make_uint2(0u, 0u)
+                       : make_uint2(narrow2<T>(sum.x * inv, sum.y * inv), narrow2<T>(sum.z * inv, sum.w * inv));
+}
+
+// ------------------------------------------------- kernels that follow closely
+// A kernel launched by launch_overlapped may start once every CTA of the one
+// before it has called let_next_kernel_start() or ended; what it reads of that
+// kernel, or of those before it, it reads after wait_for_earlier_kernels().
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                              const A &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Scores may pass the reference maximum by this many powers of two before
 // the sums are rescaled to a new one: 2^8 more in a float32 sum costs no
 // accuracy, fits float16, and most tiles then rescale nothing.

@@ -29,12 +29,15 @@
 // much error again as the rounding of the output itself, and the second
 // product is free under the loads.
 //
-// The keys of a sequence are split into chunks, one CTA each, joined by
-// merge_parts_kernel; a batch whose longest sequence is one chunk writes its
-// outputs itself.
+// The keys of all sequences and KV heads are one list of blocks of 64, dealt
+// out evenly: CTA i of N takes blocks [i*total/N, (i+1)*total/N), so one wave of
+// CTAs ends together whatever the lengths are (which only the device knows).
+// Each CTA works the list out for itself from the lengths.  A KV head that one
+// CTA has to itself is finished there; the others' parts go to merge_parts_kernel.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -75,6 +78,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
+constexpr int kUnitKeys = kSplitWarps * kBlockKeys;
+
 struct SplitArgs {
     PagedView kv;
     PagedQuery q;
@@ -82,248 +87,339 @@ struct SplitArgs {
     ScoreArgs score;
     int shared;       // keys that every sequence has at least (or none)
     int first;        // first key that this kernel reads (those before are another's)
-    int fixed;        // places of a row before those of its own part
-    int chunk;        // keys of a CTA, a multiple of kBlockKeys
     int max_len;
-    int direct;       // one part per row: write the output itself
+    int others;       // whether rows have parts of another kernel
+    size_t full_at, cta_at;
+    int2 *info;
     int *status;
 };
 
-// grid (chunks, KV heads, sequences)
+// Registers allow this many CTAs per multiprocessor.
+template <int E>
+constexpr int split_residency()
+{
+    return E <= 1 ? 6 : E <= 2 ? 5 : E <= 4 ? 4 : E <= 6 ? 3 : 2;
+}
+
+// Blocks of 64 keys that sequence b has in this kernel's list for each KV head.
+__device__ __forceinline__ int unit_count(const SplitArgs &a, int b)
+{
+    const int n = a.q.seq_lens[b];
+    return refused_length(n, a.shared, a.max_len) || n <= a.first ? 0 : (n - a.first - 1) / kUnitKeys + 1;
+}
+
 template <typename T, int E>
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(kSplitThreads, split_residency<E>())
 paged_split_kernel(const SplitArgs a)
 {
     constexpr int d = 32 * E;
     constexpr int kTilesM = d / 16;                 // m-tiles of O^T
-    constexpr bool kSplitP = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
+    __shared__ long long s_sum[kSplitWarps];
+    __shared__ long long s_before;
+    __shared__ int s_seq;
     __shared__ float s_m[kSplitWarps][8], s_l[kSplitWarps][8];
     __shared__ alignas(16) float s_o[kSplitWarps][8][d];
-    const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
-    const int G = a.q.group, n_heads = G * a.kv.n_kv_heads;
-    const int n = a.q.seq_lens[b];
-    const bool refused = n < 0 || n > a.max_len || (n > 0 && n < a.shared);
-    if (refused && threadIdx.x == 0) set_status(a.status, FATHOM_ERR_INVALID_ARG);
-    const int lo = a.first + split * a.chunk;
-    const int hi = refused ? 0 : min(n, lo + a.chunk);
-    if (lo >= hi && !(a.direct && split == 0)) return;
-
+    let_next_kernel_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    // fragments of Q: query g of the group, zeros past it
-    uint32_t qf[E][4];
-    {
-        const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + (h * G + g) * a.q.q_hs + 8 * t;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (g < G) u = *reinterpret_cast<const uint4 *>(q + 32 * j);
-            qf[j][0] = u.x; qf[j][1] = u.y; qf[j][2] = u.z; qf[j][3] = u.w;
-        }
-    }
-    float slope[2] = {0.0f, 0.0f};
-    if (a.q.slopes) {
-        if (2 * t < G) slope[0] = a.q.slopes[h * G + 2 * t] * kLog2e;
-        if (2 * t + 1 < G) slope[1] = a.q.slopes[h * G + 2 * t + 1] * kLog2e;
-    }
-    const int32_t *table = a.kv.table + (size_t)b * a.kv.table_stride;
-    const int shift = a.kv.page_shift, mask = (1 << shift) - 1;
-    const T *K = static_cast<const T *>(a.kv.k) + h * a.kv.head_stride;
-    const T *V = static_cast<const T *>(a.kv.v) + h * a.kv.head_stride;
+    const int H = a.kv.n_kv_heads, G = a.q.group, n_heads = G * H;
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float o[kTilesM][4];
+    // this CTA's run of the list: units [w, w_end), the first in sequence b,
+    // before which lie `before` units of each KV head
+    const int slice = (a.q.n_seqs + kSplitThreads - 1) / kSplitThreads;
+    const int b0 = threadIdx.x * slice, b1 = min(a.q.n_seqs, b0 + slice);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += unit_count(a, b);
+    long long upto = mine;
 #pragma unroll
-    for (int i = 0; i < kTilesM; ++i)
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+        if (lane >= off) upto += x;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    long long total = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
+    for (int x = 0; x < kSplitWarps; ++x) {
+        if (x < warp) upto += s_sum[x];
+        total += s_sum[x];
+    }
+    total *= H;
+    // as the host does for the longest lengths: at least two units a CTA, so none between two
+    // that share a row has none
+    const long long sharers = min((long long)gridDim.x, (total + 1) / 2);
+    long long w = sharers ? total * blockIdx.x / sharers : 0;
+    const long long w_end = sharers ? min(total, total * (blockIdx.x + 1) / sharers) : 0;
+    if (w >= w_end) {
+        if (a.others) wait_for_earlier_kernels();
+        return;
+    }
+    if ((upto - mine) * H <= w && w < upto * H) {
+        long long before = upto - mine;
+        int b = b0, n = unit_count(a, b);
+        while (w >= (before + n) * H) {
+            before += n;
+            n = unit_count(a, ++b);
+        }
+        s_before = before;
+        s_seq = b;
+    }
+    __syncthreads();
+    int b = s_seq;
+    long long before = s_before;
     bool bad = false;
 
-    for (int base = lo + warp * kBlockKeys; base < hi; base += kSplitWarps * kBlockKeys) {
-        // eight keys from a multiple of eight lie in one page
-        long long at[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int j = base + 8 * x;
-            const int page = j < hi ? table[j >> shift] : -1;
-            const bool ok = page >= 0 && page < a.kv.n_pages;
-            bad |= j < hi && !ok;
-            at[x] = ok ? page * a.kv.page_stride + (j & mask) * a.kv.slot_stride : -1;
+    while (w < w_end) {
+        int units = unit_count(a, b);
+        while (w >= (before + units) * H) {         // the next sequence that has keys
+            before += units;
+            units = unit_count(a, ++b);
         }
-        const bool key[2] = {at[0] >= 0 && base + g < hi, at[1] >= 0 && base + 8 + g < hi};
-        uint4 kr[2][E];
+        const int at_unit = (int)(w - before * H);
+        const int h = at_unit / units, u0 = at_unit - h * units;
+        const int u1 = (int)min((long long)units, u0 + (w_end - w));
+        w += u1 - u0;
+        const int n = a.q.seq_lens[b];
+        const int lo = a.first + u0 * kUnitKeys, hi = (int)min((long long)n, a.first + (long long)u1 * kUnitKeys);
+
+        // fragments of Q: query g of the group, zeros past it
+        uint32_t qf[E][4];
+        {
+            const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + (h * G + g) * a.q.q_hs + 8 * t;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const T *p = K + at[x] + g * a.kv.slot_stride + 8 * t;
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                kr[x][j] = key[x] ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j))
-                                  : make_uint4(0u, 0u, 0u, 0u);
-        }
-        // keys past the end are not read: what their slots hold may be anything, NaN too
-        uint32_t vr[4][(E / 2) * 4 + (E & 1) * 2];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int s = 2 * t + (x & 1);
-            const bool live = at[x >> 1] >= 0 && base + 8 * (x >> 1) + s < hi;
-            const T *p = V + at[x >> 1] + s * a.kv.slot_stride;
-#pragma unroll
-            for (int j = 0; j < E / 2; ++j) {
-                const uint4 u = live ? __ldg(reinterpret_cast<const uint4 *>(p + 64 * j + 8 * g))
-                                     : make_uint4(0u, 0u, 0u, 0u);
-                vr[x][4 * j] = u.x; vr[x][4 * j + 1] = u.y; vr[x][4 * j + 2] = u.z; vr[x][4 * j + 3] = u.w;
-            }
-            if constexpr (E & 1) {
-                const uint2 u = live ? __ldg(reinterpret_cast<const uint2 *>(p + 32 * (E - 1) + 4 * g))
-                                     : make_uint2(0u, 0u);
-                vr[x][(E / 2) * 4] = u.x; vr[x][(E / 2) * 4 + 1] = u.y;
+            for (int j = 0; j < E; ++j) {
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (g < G) u = *reinterpret_cast<const uint4 *>(q + 32 * j);
+                qf[j][0] = u.x; qf[j][1] = u.y; qf[j][2] = u.z; qf[j][3] = u.w;
             }
         }
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            mma16816<T>(c, kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y, qf[j][0], qf[j][1]);
-            mma16816<T>(c, kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w, qf[j][2], qf[j][3]);
+        float slope[2] = {0.0f, 0.0f};
+        if (a.q.slopes) {
+            if (2 * t < G) slope[0] = a.q.slopes[h * G + 2 * t] * kLog2e;
+            if (2 * t + 1 < G) slope[1] = a.q.slopes[h * G + 2 * t + 1] * kLog2e;
         }
-        // c: (key g; queries 2t, 2t+1), (key g + 8; the same)
+        const int32_t *table = a.kv.table + (size_t)b * a.kv.table_stride;
+        const int shift = a.kv.page_shift, mask = (1 << shift) - 1;
+        const T *K = static_cast<const T *>(a.kv.k) + h * a.kv.head_stride;
+        const T *V = static_cast<const T *>(a.kv.v) + h * a.kv.head_stride;
+
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float o[kTilesM][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float s = score_logit(c[x], a.score) -
-                            slope[x & 1] * (float)(n - 1 - (base + 8 * (x >> 1) + g));
-            c[x] = key[x >> 1] ? s : -INFINITY;
-        }
-        float top[2] = {fmaxf(c[0], c[2]), fmaxf(c[1], c[3])};
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale)) {
+        for (int i = 0; i < kTilesM; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
+
+        // pages of the block's halves, read one block ahead: eight keys from a
+        // multiple of eight lie in one page
+        int next[2];
+        const auto look_up = [&](int base) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) next[x] = base + 8 * x < hi ? table[(base + 8 * x) >> shift] : -1;
+        };
+        look_up(lo + warp * kBlockKeys);
+        for (int base = lo + warp * kBlockKeys; base < hi; base += kUnitKeys) {
+            long long at[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
+                const int j = base + 8 * x;
+                const bool ok = next[x] >= 0 && next[x] < a.kv.n_pages;
+                bad |= j < hi && !ok;
+                at[x] = ok ? next[x] * a.kv.page_stride + (j & mask) * a.kv.slot_stride : -1;
+            }
+            const bool key[2] = {at[0] >= 0 && base + g < hi, at[1] >= 0 && base + 8 + g < hi};
+            uint4 kr[2][E];
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1)
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], off));
-                const float next = fmaxf(m[x], top[x]);
-                const float w = m[x] == next ? 1.0f : exp2_fast(m[x] - next);
-                m[x] = next;
-                l[x] *= w;
+            for (int x = 0; x < 2; ++x) {
+                const T *p = K + at[x] + g * a.kv.slot_stride + 8 * t;
 #pragma unroll
-                for (int i = 0; i < kTilesM; ++i) {
-                    o[i][x] *= w;
-                    o[i][x + 2] *= w;
+                for (int j = 0; j < E; ++j)
+                    kr[x][j] = key[x] ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+            }
+            // keys past the end are not read: what their slots hold may be anything, NaN too
+            uint32_t vr[4][(E / 2) * 4 + (E & 1) * 2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int s = 2 * t + (x & 1);
+                const bool live = at[x >> 1] >= 0 && base + 8 * (x >> 1) + s < hi;
+                const T *p = V + at[x >> 1] + s * a.kv.slot_stride;
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) {
+                    const uint4 u = live ? __ldg(reinterpret_cast<const uint4 *>(p + 64 * j + 8 * g))
+                                         : make_uint4(0u, 0u, 0u, 0u);
+                    vr[x][4 * j] = u.x; vr[x][4 * j + 1] = u.y; vr[x][4 * j + 2] = u.z; vr[x][4 * j + 3] = u.w;
+                }
+                if constexpr (E & 1) {
+                    const uint2 u = live ? __ldg(reinterpret_cast<const uint2 *>(p + 32 * (E - 1) + 4 * g))
+                                         : make_uint2(0u, 0u);
+                    vr[x][(E / 2) * 4] = u.x; vr[x][(E / 2) * 4 + 1] = u.y;
                 }
             }
-        }
-        float p[4];
+            look_up(base + kUnitKeys);
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float ref = m[x & 1] == -INFINITY ? 0.0f : m[x & 1];
-            p[x] = exp2_fast(c[x] - ref);
-            l[x & 1] += p[x];
-        }
-        const uint32_t hi0 = narrow2<T>(p[0], p[1]), hi1 = narrow2<T>(p[2], p[3]);
-        const uint32_t b0 = transpose8x8(hi0), b1 = transpose8x8(hi1);
-        uint32_t r0 = 0u, r1 = 0u;
-        if constexpr (kSplitP) {
-            const float2 f0 = widen2<T>(hi0), f1 = widen2<T>(hi1);
-            r0 = transpose8x8(narrow2<T>(p[0] - f0.x, p[1] - f0.y));
-            r1 = transpose8x8(narrow2<T>(p[2] - f1.x, p[3] - f1.y));
-        }
+            for (int j = 0; j < E; ++j) {
+                mma16816<T>(c, kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y, qf[j][0], qf[j][1]);
+                mma16816<T>(c, kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w, qf[j][2], qf[j][3]);
+            }
+            // c: (key g; queries 2t, 2t+1), (key g + 8; the same)
 #pragma unroll
-        for (int i = 0; i < kTilesM; ++i) {
-            const uint32_t a0 = __byte_perm(vr[0][i], vr[1][i], 0x5410);
-            const uint32_t a1 = __byte_perm(vr[0][i], vr[1][i], 0x7632);
-            const uint32_t a2 = __byte_perm(vr[2][i], vr[3][i], 0x5410);
-            const uint32_t a3 = __byte_perm(vr[2][i], vr[3][i], 0x7632);
-            mma16816<T>(o[i], a0, a1, a2, a3, b0, b1);
-            if constexpr (kSplitP) mma16816<T>(o[i], a0, a1, a2, a3, r0, r1);
+            for (int x = 0; x < 4; ++x) {
+                const float s = score_logit(c[x], a.score) -
+                                slope[x & 1] * (float)(n - 1 - (base + 8 * (x >> 1) + g));
+                c[x] = key[x >> 1] ? s : -INFINITY;
+            }
+            float top[2] = {fmaxf(c[0], c[2]), fmaxf(c[1], c[3])};
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale)) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], off));
+                    const float renew = fmaxf(m[x], top[x]);
+                    const float f = m[x] == renew ? 1.0f : exp2_fast(m[x] - renew);
+                    m[x] = renew;
+                    l[x] *= f;
+#pragma unroll
+                    for (int i = 0; i < kTilesM; ++i) {
+                        o[i][x] *= f;
+                        o[i][x + 2] *= f;
+                    }
+                }
+            }
+            float p[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float ref = m[x & 1] == -INFINITY ? 0.0f : m[x & 1];
+                p[x] = exp2_fast(c[x] - ref);
+                l[x & 1] += p[x];
+            }
+            const uint32_t p0 = narrow2<T>(p[0], p[1]), p1 = narrow2<T>(p[2], p[3]);
+            const uint32_t f0 = transpose8x8(p0), f1 = transpose8x8(p1);
+            uint32_t r0 = 0u, r1 = 0u;
+            if constexpr (kSplitP) {
+                const float2 w0 = widen2<T>(p0), w1 = widen2<T>(p1);
+                r0 = transpose8x8(narrow2<T>(p[0] - w0.x, p[1] - w0.y));
+                r1 = transpose8x8(narrow2<T>(p[2] - w1.x, p[3] - w1.y));
+            }
+#pragma unroll
+            for (int i = 0; i < kTilesM; ++i) {
+                const uint32_t a0 = __byte_perm(vr[0][i], vr[1][i], 0x5410);
+                const uint32_t a1 = __byte_perm(vr[0][i], vr[1][i], 0x7632);
+                const uint32_t a2 = __byte_perm(vr[2][i], vr[3][i], 0x5410);
+                const uint32_t a3 = __byte_perm(vr[2][i], vr[3][i], 0x7632);
+                mma16816<T>(o[i], a0, a1, a2, a3, f0, f1);
+                if constexpr (kSplitP) mma16816<T>(o[i], a0, a1, a2, a3, r0, r1);
+            }
+        }
+
+        // join the warps: maxima and sums of the 8 queries, then the outputs
+        __syncthreads();                            // the last run's are read
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], off);
+            if (g == 0) {
+                s_m[warp][2 * t + x] = m[x];
+                s_l[warp][2 * t + x] = l[x];
+            }
+#pragma unroll
+            for (int i = 0; i < kTilesM; ++i) {
+                const int c0 = i < 4 * (E / 2) ? 64 * (i >> 2) + 8 * g + 2 * (i & 3)
+                                               : 32 * (E - 1) + 4 * g + 2 * (i & 3);
+                *reinterpret_cast<float2 *>(&s_o[warp][2 * t + x][c0]) = make_float2(o[i][x], o[i][x + 2]);
+            }
+        }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == units;
+        if (threadIdx.x == 0) {
+            int2 *info = a.info + (size_t)b * H + h;
+            if (u0 == 0) info->x = blockIdx.x;
+            if (u1 == units) info->y = blockIdx.x;
+        }
+        for (int i = threadIdx.x; i < G * (d / 4); i += kSplitThreads) {
+            const int qi = i / (d / 4), c0 = (i - qi * (d / 4)) * 4;
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kSplitWarps; ++x) top = fmaxf(top, s_m[x][qi]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float sum = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kSplitWarps; ++x) {
+                const float f = exp2_fast(s_m[x][qi] - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(&s_o[x][qi][c0]);
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+                sum += f * s_l[x][qi];
+            }
+            const int head = h * G + qi;
+            if (whole && !a.others) {
+                store_row<T>(a.q, b, head, c0, acc, sum);
+            } else {
+                const size_t place = whole ? a.full_at + (size_t)b * n_heads + head
+                                           : a.cta_at + (2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * (size_t)G + qi;
+                *reinterpret_cast<float4 *>(a.pv.o + place * d + c0) = acc;
+                if (c0 == 0) a.pv.ml[place] = make_float2(top, sum);
+            }
         }
     }
     if (bad) set_status(a.status, FATHOM_ERR_INVALID_ARG);
+    if (a.others) wait_for_earlier_kernels();       // so that whoever waits for this waits for those too
+}
 
-    // join the warps: maxima and sums of the 8 queries, then the outputs
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], off);
-        if (g == 0) {
-            s_m[warp][2 * t + x] = m[x];
-            s_l[warp][2 * t + x] = l[x];
-        }
-#pragma unroll
-        for (int i = 0; i < kTilesM; ++i) {
-            const int c0 = i < 4 * (E / 2) ? 64 * (i >> 2) + 8 * g + 2 * (i & 3)
-                                           : 32 * (E - 1) + 4 * g + 2 * (i & 3);
-            *reinterpret_cast<float2 *>(&s_o[warp][2 * t + x][c0]) = make_float2(o[i][x], o[i][x + 2]);
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * (d / 4); i += kSplitThreads) {
-        const int qi = i / (d / 4), c0 = (i - qi * (d / 4)) * 4;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, s_m[w][qi]);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kSplitWarps; ++w) {
-            const float f = exp2_fast(s_m[w][qi] - ref);
-            const float4 v = *reinterpret_cast<const float4 *>(&s_o[w][qi][c0]);
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-            sum += f * s_l[w][qi];
-        }
-        const int head = h * G + qi;
-        if (a.direct) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            uint16_t *out = static_cast<uint16_t *>(a.q.out) + b * a.q.out_ts + head * a.q.out_hs + c0;
-            *reinterpret_cast<uint2 *>(out) = make_uint2(narrow2<T>(acc.x * inv, acc.y * inv),
-                                                         narrow2<T>(acc.z * inv, acc.w * inv));
-        } else {
-            const size_t place = (size_t)(b * n_heads + head) * a.pv.parts + a.fixed + split;
-            *reinterpret_cast<float4 *>(a.pv.o + place * d + c0) = acc;
-            if (c0 == 0) a.pv.ml[place] = make_float2(top, sum);
-        }
-    }
+template <typename T, int E>
+cudaError_t launch_one(const SplitArgs &a, int ctas, cudaStream_t stream)
+{
+    if (a.others) return launch_overlapped(paged_split_kernel<T, E>, dim3(ctas), kSplitThreads, 0, stream, a);
+    paged_split_kernel<T, E><<<ctas, kSplitThreads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T>
-void launch_split(const SplitArgs &a, dim3 grid, cudaStream_t stream)
+cudaError_t launch_split(const SplitArgs &a, int ctas, cudaStream_t stream)
 {
     switch (a.kv.head_dim / 32) {
-    case 1: paged_split_kernel<T, 1><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    case 2: paged_split_kernel<T, 2><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    case 3: paged_split_kernel<T, 3><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    case 4: paged_split_kernel<T, 4><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    case 5: paged_split_kernel<T, 5><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    case 6: paged_split_kernel<T, 6><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    case 7: paged_split_kernel<T, 7><<<grid, kSplitThreads, 0, stream>>>(a); break;
-    default: paged_split_kernel<T, 8><<<grid, kSplitThreads, 0, stream>>>(a); break;
+    case 1: return launch_one<T, 1>(a, ctas, stream);
+    case 2: return launch_one<T, 2>(a, ctas, stream);
+    case 3: return launch_one<T, 3>(a, ctas, stream);
+    case 4: return launch_one<T, 4>(a, ctas, stream);
+    case 5: return launch_one<T, 5>(a, ctas, stream);
+    case 6: return launch_one<T, 6>(a, ctas, stream);
+    case 7: return launch_one<T, 7>(a, ctas, stream);
+    default: return launch_one<T, 8>(a, ctas, stream);
     }
 }
 
-// Keys of one CTA: enough CTAs for the GPU where the batch allows it, at least
-// one block for each warp and at most 1024 keys, so that uneven lengths even out.
-int chunk_keys(int n_kv_heads, int n_seqs, int own)
+// One wave of CTAs, or one for every 128 keys where the batch may have fewer.
+int split_ctas(int n_kv_heads, int head_dim, int n_seqs, int own)
 {
-    const long long want = (long long)own * n_kv_heads * n_seqs / (148 * 8);
-    const long long chunk = (want + 63) / 64 * 64;
-    return (int)std::min<long long>(std::max<long long>(chunk, 64), 1024);
+    constexpr int residency[8] = {split_residency<1>(), split_residency<2>(), split_residency<3>(),
+                                  split_residency<4>(), split_residency<5>(), split_residency<6>(),
+                                  split_residency<7>(), split_residency<8>()};
+    const long long units = ((long long)own + kUnitKeys - 1) / kUnitKeys * n_kv_heads * n_seqs;
+    return (int)std::min<long long>(148 * residency[head_dim / 32 - 1], (units + 1) / 2);
 }
 
 struct Plan {
     PrefixPlan prefix;
-    int first, chunk, chunks, parts, direct;
+    int first, ctas;
+    size_t full_at, cta_at, places;
 };
 Plan plan_parts(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len, int prefix_len)
 {
     Plan p{};
+    const size_t rows = (size_t)n_seqs * n_kv_heads * group;
     p.prefix = plan_prefix(n_kv_heads, head_dim, n_seqs, group, prefix_len);
     p.first = p.prefix.parts ? prefix_len : 0;
-    const int own = max_len - p.first;
-    p.chunk = chunk_keys(n_kv_heads, n_seqs, own);
-    p.chunks = (own + p.chunk - 1) / p.chunk;
-    p.parts = p.prefix.parts + p.chunks;
-    p.direct = p.parts == 1 && p.chunks == 1;
+    p.ctas = split_ctas(n_kv_heads, head_dim, n_seqs, max_len - p.first);
+    p.full_at = rows * p.prefix.parts;
+    p.cta_at = p.full_at + (p.prefix.parts ? rows : 0);
+    p.places = p.cta_at + (size_t)p.ctas * 2 * group;
     return p;
 }
 
@@ -333,42 +429,47 @@ size_t paged_attention_bytes(int n_kv_heads, int head_dim, int n_seqs, int group
                              int prefix_len)
 {
     const Plan p = plan_parts(n_kv_heads, head_dim, n_seqs, group, max_len, prefix_len);
-    return p.direct ? 0 : parts_bytes(n_seqs * n_kv_heads * group, head_dim, p.parts);
+    return parts_bytes(p.places, head_dim) + round16((size_t)n_seqs * n_kv_heads * sizeof(int2));
 }
 
 cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int max_len,
                                    int prefix_len, void *ws, cudaStream_t stream)
 {
     const Plan p = plan_parts(kv.n_kv_heads, kv.head_dim, q.n_seqs, q.group, max_len, prefix_len);
-    const int n_heads = kv.n_kv_heads * q.group;
     SplitArgs a{};
     a.kv = kv;
     a.q = q;
-    if (!p.direct) a.pv = parts_carve(ws, q.n_seqs * n_heads, kv.head_dim, p.parts);
+    a.pv = parts_carve(ws, p.places, kv.head_dim);
     a.score = score_args(q.softmax_scale, q.softcap);
     a.shared = prefix_len;
     a.first = p.first;
-    a.fixed = p.prefix.parts;
-    a.chunk = p.chunk;
     a.max_len = max_len;
-    a.direct = p.direct;
+    a.others = p.prefix.parts > 0;
+    a.full_at = p.full_at;
+    a.cta_at = p.cta_at;
+    a.info = reinterpret_cast<int2 *>(static_cast<unsigned char *>(ws) + parts_bytes(p.places, kv.head_dim));
     a.status = device_status_ptr();
-    if (p.prefix.parts) {
-        const cudaError_t e = launch_paged_prefix(kv, q, p.prefix, a.pv, prefix_len, stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (p.chunks) {
-        const dim3 grid(p.chunks, kv.n_kv_heads, q.n_seqs);
-        if (kv.dtype == FATHOM_BF16)
-            launch_split<__nv_bfloat16>(a, grid, stream);
-        else
-            launch_split<__half>(a, grid, stream);
+    cudaError_t e = cudaSuccess;
+    if (p.prefix.parts) e = launch_paged_prefix(kv, q, p.prefix, a.pv, prefix_len, stream);
+    if (e == cudaSuccess && p.ctas) {
+        e = kv.dtype == FATHOM_BF16 ? launch_split<__nv_bfloat16>(a, p.ctas, stream)
+                                    : launch_split<__half>(a, p.ctas, stream);
         note_launch();
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess || p.direct) return e;
     }
-    return launch_merge_parts(a.pv, q, n_heads, kv.head_dim, kv.dtype, a.fixed, prefix_len, a.first,
-                              p.chunk, max_len, stream);
+    if (e != cudaSuccess) return e;
+    MergeArgs m{};
+    m.pv = a.pv;
+    m.q = q;
+    m.n_heads = kv.n_kv_heads * q.group;
+    m.head_dim = kv.head_dim;
+    m.fixed = p.prefix.parts;
+    m.lens_from = p.first;
+    m.info = a.info;
+    m.full_at = p.full_at;
+    m.cta_at = p.cta_at;
+    m.shared = prefix_len;
+    m.max_len = max_len;
+    return launch_merge_parts(m, kv.dtype, stream);
 }
 
 }  // namespace fathom

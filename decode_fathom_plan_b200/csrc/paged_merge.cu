@@ -3,7 +3,11 @@
 // Part p of a row holds a_p = sum_j 2^(s_j - m_p) V_j and l_p = sum_j
 // 2^(s_j - m_p); the row is sum_p 2^(m_p - M) a_p / sum_p 2^(m_p - M) l_p with
 // M = max m_p.  One CTA per row: d/4 lanes of 16-byte loads by as many part
-// groups as fit, summed through shared memory in a fixed order.
+// groups as fit, each with a running maximum over four parts at a time, so
+// that a row of 32 parts costs one round of loads; the groups are summed
+// through shared memory in a fixed order.
+// It is launched while the kernels before it run (programmatic dependent
+// launch) and waits for them: back to back 2 us a call less.
 #include <math.h>
 
 #include "paged.cuh"
@@ -11,109 +15,140 @@
 namespace fathom {
 namespace {
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
+constexpr int kAtOnce = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads)
-merge_parts_kernel(const PartsView pv, const PagedQuery q, int n_heads, int d, int fixed, int shared,
-                   int first, int chunk, int max_len, int *status)
+merge_parts_kernel(const MergeArgs a)
 {
-    __shared__ float s_m[kMergeThreads / 32];
     __shared__ float4 s_o[kMergeThreads];
-    __shared__ float s_l[kMergeThreads];
-    const int row = blockIdx.x, b = row / n_heads, head = row - b * n_heads;
-    int parts = pv.parts;
-    if (chunk) {
-        const int n = q.seq_lens[b];
-        const bool refused = n < 0 || n > max_len || (n > 0 && n < shared);
-        if (refused && threadIdx.x == 0) set_status(status, FATHOM_ERR_INVALID_ARG);
-        parts = (n == 0 || refused) ? 0 : fixed + (n - first + chunk - 1) / chunk;
+    __shared__ float s_m[kMergeThreads], s_l[kMergeThreads];
+    const int row = blockIdx.x, b = row / a.n_heads, head = row - b * a.n_heads;
+    const int d = a.head_dim;
+    wait_for_earlier_kernels();
+    int own = 0;                       // parts behind the fixed ones
+    size_t own_at = 0;                 // place of the first
+    bool joined = false;               // the row's own keys are one part
+    int fixed = a.fixed;
+    if (a.lens_from >= 0) {
+        const int n = a.q.seq_lens[b];
+        if (refused_length(n, a.shared, a.max_len)) {
+            if (threadIdx.x == 0) set_status(a.status, FATHOM_ERR_INVALID_ARG);
+            fixed = 0;
+        } else if (n == 0) {
+            fixed = 0;
+        } else if (n > a.lens_from) {
+            const int h = head / a.q.group, g = head - h * a.q.group;
+            const int2 ctas = a.info[(size_t)b * (a.n_heads / a.q.group) + h];
+            if (ctas.x == ctas.y) {
+                if (!a.fixed) return;  // written by the CTA that had it all
+                joined = true;
+                own = 1;
+                own_at = a.full_at + row;
+            } else {
+                own = ctas.y - ctas.x + 1;
+                own_at = a.cta_at + (size_t)ctas.x * 2 * a.q.group + g;
+            }
+        }
     }
-    const float2 *ml = pv.ml + (size_t)row * pv.parts;
-    float m = -INFINITY;
-    for (int p = threadIdx.x; p < parts; p += kMergeThreads) m = fmaxf(m, ml[p].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-    if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = s_m[0];
-#pragma unroll
-    for (int w = 1; w < kMergeThreads / 32; ++w) m = fmaxf(m, s_m[w]);
-    const float ref = m == -INFINITY ? 0.0f : m;
+    const int parts = fixed + own;
+    // of the CTAs that share a row the first keeps its part in its second
+    // place (the row begins there), the others in their first
+    const auto place = [&](int p) -> size_t {
+        if (p < fixed) return (size_t)row * a.fixed + p;
+        if (joined) return own_at;
+        p -= fixed;
+        return own_at + (size_t)(2 * p + (p == 0 ? 1 : 0)) * a.q.group;
+    };
 
     const int lanes = d / 4, groups = kMergeThreads / lanes;
     const int grp = threadIdx.x / lanes, lane = threadIdx.x - grp * lanes;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     if (grp < groups) {
-        const float4 *o = reinterpret_cast<const float4 *>(pv.o + (size_t)row * pv.parts * d);
-#pragma unroll 4
-        for (int p = grp; p < parts; p += groups) {
-            const float2 x = ml[p];
-            if (x.x == -INFINITY && x.y == 0.0f) continue;   // no key, and no sum written
-            const float4 v = o[(size_t)p * lanes + lane];
-            const float w = exp2_fast(x.x - ref);
-            acc.x += w * v.x;
-            acc.y += w * v.y;
-            acc.z += w * v.z;
-            acc.w += w * v.w;
-            l += w * x.y;
+        for (int p0 = grp; p0 < parts; p0 += kAtOnce * groups) {
+            float2 x[kAtOnce];
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int p = p0 + u * groups;
+                x[u] = make_float2(-INFINITY, 0.0f);
+                if (p < parts) {
+                    const size_t at = place(p);
+                    x[u] = a.pv.ml[at];
+                    v[u] = reinterpret_cast<const float4 *>(a.pv.o)[at * lanes + lane];
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, x[u].x);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float w = exp2_fast(m - ref);
+            acc.x *= w;
+            acc.y *= w;
+            acc.z *= w;
+            acc.w *= w;
+            l *= w;
+            m = top;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if (x[u].x == -INFINITY && x[u].y == 0.0f) continue;   // no key, and no sum written
+                w = exp2_fast(x[u].x - ref);
+                acc.x += w * v[u].x;
+                acc.y += w * v[u].y;
+                acc.z += w * v[u].z;
+                acc.w += w * v[u].w;
+                l += w * x[u].y;
+            }
         }
     }
     s_o[threadIdx.x] = acc;
+    s_m[threadIdx.x] = m;
     s_l[threadIdx.x] = l;
     __syncthreads();
     if (grp != 0) return;
-    for (int g = 1; g < groups; ++g) {
+    float top = m;
+    for (int g = 1; g < groups; ++g) top = fmaxf(top, s_m[g * lanes + lane]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    l = 0.0f;
+    for (int g = 0; g < groups; ++g) {
+        const float w = exp2_fast(s_m[g * lanes + lane] - ref);
         const float4 v = s_o[g * lanes + lane];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-        l += s_l[g * lanes + lane];
+        acc.x += w * v.x;
+        acc.y += w * v.y;
+        acc.z += w * v.z;
+        acc.w += w * v.w;
+        l += w * s_l[g * lanes + lane];
     }
-    // l is 0 only where no key took part (the key that set a part's maximum weighs 1 in it),
-    // NaN if a score was
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *out = static_cast<uint16_t *>(q.out) + b * q.out_ts + head * q.out_hs;
-    *reinterpret_cast<uint2 *>(out + lane * 4) =
-        l == 0.0f ? make_uint2(0u, 0u)
-                  : make_uint2(narrow2<T>(acc.x * inv, acc.y * inv), narrow2<T>(acc.z * inv, acc.w * inv));
+    store_row<T>(a.q, b, head, lane * 4, acc, l);
 }
-
-size_t round16(size_t b) { return (b + 15) & ~(size_t)15; }
 
 }  // namespace
 
-size_t parts_bytes(int rows, int head_dim, int parts)
+size_t round16(size_t b) { return (b + 15) & ~(size_t)15; }
+
+size_t parts_bytes(size_t places, int head_dim)
 {
-    return round16((size_t)rows * parts * head_dim * sizeof(float)) +
-           round16((size_t)rows * parts * sizeof(float2));
+    return places * head_dim * sizeof(float) + round16(places * sizeof(float2));
 }
 
-PartsView parts_carve(void *ws, int rows, int head_dim, int parts)
+PartsView parts_carve(void *ws, size_t places, int head_dim)
 {
-    PartsView pv{};
-    pv.o = static_cast<float *>(ws);
-    pv.ml = reinterpret_cast<float2 *>(static_cast<unsigned char *>(ws) +
-                                       round16((size_t)rows * parts * head_dim * sizeof(float)));
-    pv.parts = parts;
-    return pv;
+    float *o = static_cast<float *>(ws);
+    return PartsView{o, reinterpret_cast<float2 *>(o + places * head_dim)};
 }
 
-cudaError_t launch_merge_parts(const PartsView &pv, const PagedQuery &q, int n_heads, int head_dim,
-                               int dtype, int fixed, int shared, int first, int chunk,
-                               int max_len, cudaStream_t stream)
+cudaError_t launch_merge_parts(const MergeArgs &args, int dtype, cudaStream_t stream)
 {
-    const int rows = q.n_seqs * n_heads;
-    if (dtype == FATHOM_BF16)
-        merge_parts_kernel<__nv_bfloat16><<<rows, kMergeThreads, 0, stream>>>(
-            pv, q, n_heads, head_dim, fixed, shared, first, chunk, max_len, device_status_ptr());
-    else
-        merge_parts_kernel<__half><<<rows, kMergeThreads, 0, stream>>>(
-            pv, q, n_heads, head_dim, fixed, shared, first, chunk, max_len, device_status_ptr());
+    MergeArgs a = args;
+    a.status = device_status_ptr();
     note_launch();
-    return cudaGetLastError();
+    const int rows = a.q.n_seqs * a.n_heads;
+    return dtype == FATHOM_BF16
+               ? launch_overlapped(merge_parts_kernel<__nv_bfloat16>, dim3(rows), kMergeThreads, 0, stream, a)
+               : launch_overlapped(merge_parts_kernel<__half>, dim3(rows), kMergeThreads, 0, stream, a);
 }
 
 }  // namespace fathom

@@ -55,7 +55,7 @@ struct PrefixArgs {
     ScoreArgs score;
     const int32_t *table;                        // the first row of the page table
     int n_heads, n_pages, page_shift, head_dim, is_bf16;
-    int prefix_len, rows, n_tiles, splits, row_groups, two_blocks;
+    int prefix_len, rows, n_tiles, splits, row_groups, two_blocks, parts;
     int *status;
 };
 
@@ -214,6 +214,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 {
     using Shape = PrefixShape<NB>;
     constexpr int kSlots = Shape::kSlots, kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
+    let_next_kernel_start();
     extern __shared__ unsigned char s_raw[];
     __shared__ alignas(8) uint64_t s_bar[2 * kStages + 3 * kSlots + 1];
     __shared__ uint32_t s_tmem;
@@ -468,7 +469,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if (ok && live) {
             tc_after();
             const int part = shared ? split : split * kSlots + s;
-            const size_t place = (size_t)(b * a.n_heads + head) * a.pv.parts + part;
+            const size_t place = (size_t)(b * a.n_heads + head) * a.parts + part;
             if (count > 0) {
                 for (int c = 0; c < d; c += 32) {
                     float o[32];
@@ -585,6 +586,7 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.splits = p.splits;
     a.row_groups = p.row_groups;
     a.two_blocks = p.two_blocks;
+    a.parts = p.parts;
     a.status = device_status_ptr();
     const int ctas = p.row_groups * kv.n_kv_heads * p.splits;
     switch ((kv.head_dim + 63) / 64) {

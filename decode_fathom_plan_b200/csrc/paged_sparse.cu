@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kSparseThreads)
 paged_sparse_kernel(const SparseArgs a)
 {
     constexpr int d = 32 * E;
+    let_next_kernel_start();
     __shared__ float s_m[kSparseWarps], s_l[kSparseWarps];
     __shared__ alignas(16) float s_o[kSparseWarps][d];
     const int b = blockIdx.z, head = blockIdx.y, run = blockIdx.x, n_heads = gridDim.y;
@@ -172,12 +173,9 @@ paged_sparse_kernel(const SparseArgs a)
         sum += f * s_l[x];
     }
     if (a.direct) {
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint16_t *out = static_cast<uint16_t *>(a.q.out) + b * a.q.out_ts + head * a.q.out_hs + c0;
-        *reinterpret_cast<uint2 *>(out) = make_uint2(narrow2<T>(acc.x * inv, acc.y * inv),
-                                                     narrow2<T>(acc.z * inv, acc.w * inv));
+        store_row<T>(a.q, b, head, c0, acc, sum);
     } else {
-        const size_t place = ((size_t)b * n_heads + head) * a.pv.parts + run;
+        const size_t place = ((size_t)b * n_heads + head) * gridDim.x + run;
         *reinterpret_cast<float4 *>(a.pv.o + place * d + c0) = acc;
         if (c0 == 0) a.pv.ml[place] = make_float2(top, sum);
     }
@@ -204,7 +202,7 @@ int sparse_runs(int k) { return (k - 1) / kRunKeys + 1; }
 
 size_t paged_sparse_bytes(int n_rows, int head_dim, int k)
 {
-    return sparse_runs(k) == 1 ? 0 : parts_bytes(n_rows, head_dim, sparse_runs(k));
+    return sparse_runs(k) == 1 ? 0 : parts_bytes((size_t)n_rows * sparse_runs(k), head_dim);
 }
 
 cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const int32_t *idx, int k,
@@ -218,7 +216,7 @@ cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const 
     a.idx = idx;
     a.k = k;
     a.direct = runs == 1;
-    if (!a.direct) a.pv = parts_carve(ws, q.n_seqs * n_heads, kv.head_dim, runs);
+    if (!a.direct) a.pv = parts_carve(ws, (size_t)q.n_seqs * n_heads * runs, kv.head_dim);
     a.status = device_status_ptr();
     const dim3 grid(runs, n_heads, q.n_seqs);
     if (kv.dtype == FATHOM_BF16)
@@ -228,7 +226,14 @@ cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const 
     note_launch();
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.direct) return e;
-    return launch_merge_parts(a.pv, q, n_heads, kv.head_dim, kv.dtype, 0, 0, 0, 0, 0, stream);
+    MergeArgs m{};
+    m.pv = a.pv;
+    m.q = q;
+    m.n_heads = n_heads;
+    m.head_dim = kv.head_dim;
+    m.fixed = runs;
+    m.lens_from = -1;
+    return launch_merge_parts(m, kv.dtype, stream);
 }
 
 }  // namespace fathom
