@@ -80,6 +80,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 
 constexpr int kUnitKeys = kSplitWarps * kBlockKeys;
 
+// A 16-byte load from shared memory that stays where it is written.
+__device__ __forceinline__ uint4 load_shared(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+    return v;
+}
+
 struct SplitArgs {
     PagedView kv;
     PagedQuery q;
@@ -98,7 +108,7 @@ struct SplitArgs {
 template <int E>
 constexpr int split_residency()
 {
-    return E <= 1 ? 6 : E <= 2 ? 5 : E <= 4 ? 4 : E <= 6 ? 3 : 2;
+    return E <= 2 ? 5 : E <= 4 ? 4 : E <= 6 ? 3 : 2;
 }
 
 // Blocks of 64 keys that sequence b has in this kernel's list for each KV head.
@@ -115,11 +125,18 @@ paged_split_kernel(const SplitArgs a)
     constexpr int d = 32 * E;
     constexpr int kTilesM = d / 16;                 // m-tiles of O^T
     constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int kWordsV = (E / 2) * 4 + (E & 1) * 2;
+    // What a warp loads at a time, 4 KB or more, must fit the registers with the accumulators: wide
+    // heads keep Q's fragments (the same for every warp) in shared memory, narrow ones take
+    // several blocks of keys.
+    constexpr bool kSharedQ = E >= 3;
+    constexpr int KB = E == 1 ? 2 : 1;
     __shared__ long long s_sum[kSplitWarps];
     __shared__ long long s_before;
     __shared__ int s_seq;
     __shared__ float s_m[kSplitWarps][8], s_l[kSplitWarps][8];
     __shared__ alignas(16) float s_o[kSplitWarps][8][d];
+    __shared__ uint4 s_q[kSharedQ ? E : 1][32];
     let_next_kernel_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -146,9 +163,8 @@ paged_split_kernel(const SplitArgs a)
         total += s_sum[x];
     }
     total *= H;
-    // as the host does for the longest lengths: at least two units a CTA, so none between two
-    // that share a row has none
-    const long long sharers = min((long long)gridDim.x, (total + 1) / 2);
+    // at least a unit a CTA, so that none between two that share a row has none
+    const long long sharers = min((long long)gridDim.x, total);
     long long w = sharers ? total * blockIdx.x / sharers : 0;
     const long long w_end = sharers ? min(total, total * (blockIdx.x + 1) / sharers) : 0;
     if (w >= w_end) {
@@ -184,16 +200,20 @@ paged_split_kernel(const SplitArgs a)
         const int lo = a.first + u0 * kUnitKeys, hi = (int)min((long long)n, a.first + (long long)u1 * kUnitKeys);
 
         // fragments of Q: query g of the group, zeros past it
-        uint32_t qf[E][4];
-        {
+        uint4 qr[kSharedQ ? 1 : E];
+        __syncthreads();                            // the last run's, and its outputs, are read
+        if (!kSharedQ || warp == 0) {
             const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + (h * G + g) * a.q.q_hs + 8 * t;
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (g < G) u = *reinterpret_cast<const uint4 *>(q + 32 * j);
-                qf[j][0] = u.x; qf[j][1] = u.y; qf[j][2] = u.z; qf[j][3] = u.w;
+            for (int e = 0; e < E; ++e) {
+                const uint4 w4 = g < G ? *reinterpret_cast<const uint4 *>(q + 32 * e) : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kSharedQ)
+                    s_q[e][lane] = w4;
+                else
+                    qr[e] = w4;
             }
         }
+        if (kSharedQ) __syncthreads();
         float slope[2] = {0.0f, 0.0f};
         if (a.q.slopes) {
             if (2 * t < G) slope[0] = a.q.slopes[h * G + 2 * t] * kLog2e;
@@ -211,67 +231,82 @@ paged_split_kernel(const SplitArgs a)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
 
-        // pages of the block's halves, read one block ahead: eight keys from a
+        // pages of the blocks' halves, read one step ahead: eight keys from a
         // multiple of eight lie in one page
-        int next[2];
+        int next[KB][2];
         const auto look_up = [&](int base) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) next[x] = base + 8 * x < hi ? table[(base + 8 * x) >> shift] : -1;
+            for (int u = 0; u < KB; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = base + u * kUnitKeys + 8 * x;
+                    next[u][x] = j < hi ? table[j >> shift] : -1;
+                }
         };
         look_up(lo + warp * kBlockKeys);
-        for (int base = lo + warp * kBlockKeys; base < hi; base += kUnitKeys) {
-            long long at[2];
+        for (int base = lo + warp * kBlockKeys; base < hi; base += KB * kUnitKeys) {
+            bool key[KB][2];
+            uint4 kr[KB][2][E];
+            uint32_t vr[KB][4][kWordsV];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int j = base + 8 * x;
-                const bool ok = next[x] >= 0 && next[x] < a.kv.n_pages;
-                bad |= j < hi && !ok;
-                at[x] = ok ? next[x] * a.kv.page_stride + (j & mask) * a.kv.slot_stride : -1;
-            }
-            const bool key[2] = {at[0] >= 0 && base + g < hi, at[1] >= 0 && base + 8 + g < hi};
-            uint4 kr[2][E];
+            for (int u = 0; u < KB; ++u) {
+                const int j0 = base + u * kUnitKeys;
+                long long at[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const T *p = K + at[x] + g * a.kv.slot_stride + 8 * t;
+                for (int x = 0; x < 2; ++x) {
+                    const int j = j0 + 8 * x;
+                    const bool ok = next[u][x] >= 0 && next[u][x] < a.kv.n_pages;
+                    bad |= j < hi && !ok;
+                    at[x] = ok ? next[u][x] * a.kv.page_stride + (j & mask) * a.kv.slot_stride : -1;
+                    key[u][x] = ok && j + g < hi;
+                    const T *p = K + at[x] + g * a.kv.slot_stride + 8 * t;
 #pragma unroll
-                for (int j = 0; j < E; ++j)
-                    kr[x][j] = key[x] ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * j))
-                                      : make_uint4(0u, 0u, 0u, 0u);
-            }
-            // keys past the end are not read: what their slots hold may be anything, NaN too
-            uint32_t vr[4][(E / 2) * 4 + (E & 1) * 2];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int s = 2 * t + (x & 1);
-                const bool live = at[x >> 1] >= 0 && base + 8 * (x >> 1) + s < hi;
-                const T *p = V + at[x >> 1] + s * a.kv.slot_stride;
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    const uint4 u = live ? __ldg(reinterpret_cast<const uint4 *>(p + 64 * j + 8 * g))
-                                         : make_uint4(0u, 0u, 0u, 0u);
-                    vr[x][4 * j] = u.x; vr[x][4 * j + 1] = u.y; vr[x][4 * j + 2] = u.z; vr[x][4 * j + 3] = u.w;
+                    for (int e = 0; e < E; ++e)
+                        kr[u][x][e] = key[u][x] ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * e))
+                                                : make_uint4(0u, 0u, 0u, 0u);
                 }
-                if constexpr (E & 1) {
-                    const uint2 u = live ? __ldg(reinterpret_cast<const uint2 *>(p + 32 * (E - 1) + 4 * g))
-                                         : make_uint2(0u, 0u);
-                    vr[x][(E / 2) * 4] = u.x; vr[x][(E / 2) * 4 + 1] = u.y;
+                // keys past the end are not read: what their slots hold may be anything, NaN too
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int s = 2 * t + (x & 1);
+                    const bool live = at[x >> 1] >= 0 && j0 + 8 * (x >> 1) + s < hi;
+                    const T *p = V + at[x >> 1] + s * a.kv.slot_stride;
+                    uint32_t *to = vr[u][x];
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        const uint4 w4 = live ? __ldg(reinterpret_cast<const uint4 *>(p + 64 * e + 8 * g))
+                                              : make_uint4(0u, 0u, 0u, 0u);
+                        to[4 * e] = w4.x; to[4 * e + 1] = w4.y; to[4 * e + 2] = w4.z; to[4 * e + 3] = w4.w;
+                    }
+                    if constexpr (E & 1) {
+                        const uint2 w2 = live ? __ldg(reinterpret_cast<const uint2 *>(p + 32 * (E - 1) + 4 * g))
+                                              : make_uint2(0u, 0u);
+                        to[kWordsV - 2] = w2.x; to[kWordsV - 1] = w2.y;
+                    }
                 }
             }
-            look_up(base + kUnitKeys);
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                mma16816<T>(c, kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y, qf[j][0], qf[j][1]);
-                mma16816<T>(c, kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w, qf[j][2], qf[j][3]);
-            }
+            look_up(base + KB * kUnitKeys);
             // c: (key g; queries 2t, 2t+1), (key g + 8; the same)
+            float c[KB][4];
+            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float s = score_logit(c[x], a.score) -
-                                slope[x & 1] * (float)(n - 1 - (base + 8 * (x >> 1) + g));
-                c[x] = key[x >> 1] ? s : -INFINITY;
+            for (int u = 0; u < KB; ++u) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) c[u][x] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const uint4 q4 = kSharedQ ? load_shared(&s_q[kSharedQ ? e : 0][lane]) : qr[kSharedQ ? 0 : e];
+                    mma16816<T>(c[u], kr[u][0][e].x, kr[u][1][e].x, kr[u][0][e].y, kr[u][1][e].y, q4.x, q4.y);
+                    mma16816<T>(c[u], kr[u][0][e].z, kr[u][1][e].z, kr[u][0][e].w, kr[u][1][e].w, q4.z, q4.w);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float s = score_logit(c[u][x], a.score) -
+                                    slope[x & 1] * (float)(n - 1 - (base + u * kUnitKeys + 8 * (x >> 1) + g));
+                    c[u][x] = key[u][x >> 1] ? s : -INFINITY;
+                    top[x & 1] = fmaxf(top[x & 1], c[u][x]);
+                }
             }
-            float top[2] = {fmaxf(c[0], c[2]), fmaxf(c[1], c[3])};
             if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale)) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -289,34 +324,36 @@ paged_split_kernel(const SplitArgs a)
                     }
                 }
             }
-            float p[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float ref = m[x & 1] == -INFINITY ? 0.0f : m[x & 1];
-                p[x] = exp2_fast(c[x] - ref);
-                l[x & 1] += p[x];
-            }
-            const uint32_t p0 = narrow2<T>(p[0], p[1]), p1 = narrow2<T>(p[2], p[3]);
-            const uint32_t f0 = transpose8x8(p0), f1 = transpose8x8(p1);
-            uint32_t r0 = 0u, r1 = 0u;
-            if constexpr (kSplitP) {
-                const float2 w0 = widen2<T>(p0), w1 = widen2<T>(p1);
-                r0 = transpose8x8(narrow2<T>(p[0] - w0.x, p[1] - w0.y));
-                r1 = transpose8x8(narrow2<T>(p[2] - w1.x, p[3] - w1.y));
-            }
+            for (int u = 0; u < KB; ++u) {
+                float p[4];
 #pragma unroll
-            for (int i = 0; i < kTilesM; ++i) {
-                const uint32_t a0 = __byte_perm(vr[0][i], vr[1][i], 0x5410);
-                const uint32_t a1 = __byte_perm(vr[0][i], vr[1][i], 0x7632);
-                const uint32_t a2 = __byte_perm(vr[2][i], vr[3][i], 0x5410);
-                const uint32_t a3 = __byte_perm(vr[2][i], vr[3][i], 0x7632);
-                mma16816<T>(o[i], a0, a1, a2, a3, f0, f1);
-                if constexpr (kSplitP) mma16816<T>(o[i], a0, a1, a2, a3, r0, r1);
+                for (int x = 0; x < 4; ++x) {
+                    const float ref = m[x & 1] == -INFINITY ? 0.0f : m[x & 1];
+                    p[x] = exp2_fast(c[u][x] - ref);
+                    l[x & 1] += p[x];
+                }
+                const uint32_t p0 = narrow2<T>(p[0], p[1]), p1 = narrow2<T>(p[2], p[3]);
+                const uint32_t f0 = transpose8x8(p0), f1 = transpose8x8(p1);
+                uint32_t r0 = 0u, r1 = 0u;
+                if constexpr (kSplitP) {
+                    const float2 w0 = widen2<T>(p0), w1 = widen2<T>(p1);
+                    r0 = transpose8x8(narrow2<T>(p[0] - w0.x, p[1] - w0.y));
+                    r1 = transpose8x8(narrow2<T>(p[2] - w1.x, p[3] - w1.y));
+                }
+#pragma unroll
+                for (int i = 0; i < kTilesM; ++i) {
+                    const uint32_t a0 = __byte_perm(vr[u][0][i], vr[u][1][i], 0x5410);
+                    const uint32_t a1 = __byte_perm(vr[u][0][i], vr[u][1][i], 0x7632);
+                    const uint32_t a2 = __byte_perm(vr[u][2][i], vr[u][3][i], 0x5410);
+                    const uint32_t a3 = __byte_perm(vr[u][2][i], vr[u][3][i], 0x7632);
+                    mma16816<T>(o[i], a0, a1, a2, a3, f0, f1);
+                    if constexpr (kSplitP) mma16816<T>(o[i], a0, a1, a2, a3, r0, r1);
+                }
             }
         }
 
         // join the warps: maxima and sums of the 8 queries, then the outputs
-        __syncthreads();                            // the last run's are read
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
@@ -395,14 +432,14 @@ cudaError_t launch_split(const SplitArgs &a, int ctas, cudaStream_t stream)
     }
 }
 
-// One wave of CTAs, or one for every 128 keys where the batch may have fewer.
+// One wave of CTAs, or one for every 64 keys where the batch may have fewer.
 int split_ctas(int n_kv_heads, int head_dim, int n_seqs, int own)
 {
     constexpr int residency[8] = {split_residency<1>(), split_residency<2>(), split_residency<3>(),
                                   split_residency<4>(), split_residency<5>(), split_residency<6>(),
                                   split_residency<7>(), split_residency<8>()};
     const long long units = ((long long)own + kUnitKeys - 1) / kUnitKeys * n_kv_heads * n_seqs;
-    return (int)std::min<long long>(148 * residency[head_dim / 32 - 1], (units + 1) / 2);
+    return (int)std::min<long long>(148 * residency[head_dim / 32 - 1], units);
 }
 
 struct Plan {

@@ -32,15 +32,15 @@ merge_parts_kernel(const MergeArgs a)
     bool joined = false;               // the row's own keys are one part
     int fixed = a.fixed;
     if (a.lens_from >= 0) {
+        const int h = head / a.q.group, g = head - h * a.q.group;
         const int n = a.q.seq_lens[b];
+        const int2 ctas = a.info[(size_t)b * (a.n_heads / a.q.group) + h];   // not written where no keys are
         if (refused_length(n, a.shared, a.max_len)) {
             if (threadIdx.x == 0) set_status(a.status, FATHOM_ERR_INVALID_ARG);
             fixed = 0;
         } else if (n == 0) {
             fixed = 0;
         } else if (n > a.lens_from) {
-            const int h = head / a.q.group, g = head - h * a.q.group;
-            const int2 ctas = a.info[(size_t)b * (a.n_heads / a.q.group) + h];
             if (ctas.x == ctas.y) {
                 if (!a.fixed) return;  // written by the CTA that had it all
                 joined = true;
