@@ -28,6 +28,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -54,7 +55,7 @@ struct PrefixArgs {
     PartsView pv;
     ScoreArgs score;
     const int32_t *table;                        // the first row of the page table
-    int n_heads, n_pages, page_shift, head_dim, is_bf16;
+    int n_heads, n_pages, page_shift, head_dim;
     int prefix_len, rows, n_tiles, splits, row_groups, two_blocks, parts;
     int *status;
 };
@@ -170,6 +171,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *x)
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float *x)
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float *x)
 {
     const uint32_t *r = reinterpret_cast<const uint32_t *>(x);
@@ -193,6 +205,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
         : "memory");
 }
 
+// Whole 32-byte sectors: each lane writes another row.
+__device__ __forceinline__ void store8(float *p, const float *x)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]),
+                 "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
 // Walks the steps (iteration, slot) of a CTA in the order in which their
 // tiles are consumed; the copying and the issuing warp follow the same walk.
 // At each step comes first V of the slot's previous tile, then K of its next.
@@ -207,7 +227,7 @@ struct Walk {
 };
 
 // grid: (row group, KV head) fastest, then the run of tiles
-template <int NB>
+template <typename T, int NB>
 __global__ void __launch_bounds__(PrefixShape<NB>::kThreads, 1)
 paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const PrefixArgs a)
@@ -216,15 +236,14 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     constexpr int kSlots = Shape::kSlots, kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
     let_next_kernel_start();
     extern __shared__ unsigned char s_raw[];
-    __shared__ alignas(8) uint64_t s_bar[2 * kStages + 3 * kSlots + 1];
+    __shared__ alignas(8) uint64_t s_bar[2 * kStages + 3 * kSlots + 2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
-    unsigned char *const s_q = s_raw + (base - smem_u32(s_raw));
     const uint32_t q_addr = base, ring = base + kSlots * kTileBytes;
     const uint32_t full = smem_u32(s_bar), empty = full + 8 * kStages, s_ready = empty + 8 * kStages,
                    p_ready = s_ready + 8 * kSlots, o_ready = p_ready + 8 * kSlots,
-                   drained = o_ready + 8 * kSlots;
+                   q_ready = o_ready + 8 * kSlots, drained = q_ready + 8;
 
     const int per = gridDim.x / a.splits;                       // row groups * KV heads
     const int split = blockIdx.x / per, unit = blockIdx.x - split * per;
@@ -249,6 +268,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             mbar_init(p_ready + 8 * s, 4);
             mbar_init(o_ready + 8 * s, 1);
         }
+        mbar_init(q_ready, 4 * kSlots);
         mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -258,23 +278,6 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                      "n"(kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    // Q rows of the slots into their swizzled tiles, zeros past the last row
-    {
-        const uint16_t *q = static_cast<const uint16_t *>(a.q.q);
-        const int chunks = d / 8, rows = kRows * (shared ? kSlots : 1);
-        for (int i = threadIdx.x; i < rows * chunks; i += Shape::kThreads) {
-            const int r = i / chunks, c = i - r * chunks, row = row0 + r;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (row < a.rows) {
-                const int b = row / G;
-                u = *reinterpret_cast<const uint4 *>(q + b * a.q.q_ts + (h * G + row - b * G) * a.q.q_hs + 8 * c);
-            }
-            const int x = r & (kRows - 1);
-            *reinterpret_cast<uint4 *>(s_q + (r / kRows) * kTileBytes + (c >> 3) * kBlockBytes + x * 128 +
-                                       (((c & 7) ^ (x & 7)) << 4)) = u;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     tc_before();
     __syncthreads();
@@ -330,12 +333,12 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     } else if (warp == 1) {
         // ---------------------------------------------------- products
         if (lane == 0) {
-            const uint32_t type = a.is_bf16 ? 1u : 0u;
+            const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((128u >> 4) << 24);
             const uint32_t idesc_qk = common | ((uint32_t)(kTile >> 3) << 17);
             const uint32_t idesc_pv = common | (1u << 16) | ((uint32_t)(d >> 3) << 17);
             int used = 0, k_stage = 0, v_stage = 0, k_use = 0, v_use = 0;
-            bool ok = true;
+            bool ok = mbar_wait(q_ready, 0, stop);
             const int n = walk.iterations();
             for (int i = 0; i <= n && ok; ++i)
                 for (int s = 0; s < kSlots && ok; ++s) {
@@ -389,6 +392,37 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const int row = row0 + (shared ? s * kRows : 0) + r;
         const bool live = row - lane < a.rows;                  // of the warp: any row at all
         const int b = min(row, a.rows - 1) / G, head = h * G + min(row, a.rows - 1) - b * G;
+        {
+            // the warp's 32 rows of Q into their swizzled tile; slots with the same rows take turns
+            const long long mine = b * a.q.q_ts + head * a.q.q_hs;
+            const uint16_t *q = static_cast<const uint16_t *>(a.q.q);
+            const uint32_t to = q_addr + (shared ? s * kTileBytes : 0);
+            constexpr int kChunks = NB * 8, kBatch = 8;
+            const int first = shared ? 0 : s, step = shared ? 1 : kSlots;
+            for (int i0 = first; i0 < kChunks; i0 += kBatch * step) {
+                uint4 u[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + k * step, x = (i * 32 + lane) / kChunks, c = (i * 32 + lane) - x * kChunks;
+                    const long long off = __shfl_sync(0xFFFFFFFFu, mine, x & 31);
+                    u[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < kChunks && c * 8 < d && live) u[k] = *reinterpret_cast<const uint4 *>(q + off + 8 * c);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + k * step, x = (i * 32 + lane) / kChunks, c = (i * 32 + lane) - x * kChunks;
+                    const int at = (warp & 3) * 32 + x;
+                    if (i < kChunks)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         to + (c >> 3) * kBlockBytes + at * 128 + (((c & 7) ^ (at & 7)) << 4)),
+                                     "r"(u[k].x), "r"(u[k].y), "r"(u[k].z), "r"(u[k].w)
+                                     : "memory");
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
+        }
         const int seq_len = a.q.seq_lens[b];
         const float slope = a.q.slopes ? a.q.slopes[head] * kLog2e : 0.0f;
         const bool plain = a.score.cap == 0.0f && !a.q.slopes && a.score.scale > 0.0f;
@@ -403,26 +437,34 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             if (!ok) break;
             tc_after();
             if (live) {
-                float x[kTile];
-#pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, x + c);
-                tc_wait_ld();
+                // Twice over the row, 32 columns at a time and the next ones on their way: the
+                // maximum, then the probabilities.  (A row held in registers would be 128 of them.)
                 const int key0 = (t0 + walk.tile(i, s)) * kTile;
                 const int valid = a.prefix_len - key0;          // keys of this tile
-                float mult = a.score.scale;
-                if (!plain || valid < kTile) {
-                    const float dist = (float)(seq_len - 1 - key0);
+                const bool as_is = plain && valid >= kTile;
+                const float mult = as_is ? a.score.scale : 1.0f;
+                const float dist = (float)(seq_len - 1 - key0);
+                float x[2][32];
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld32(s_addr, x[0]);
 #pragma unroll
-                    for (int j = 0; j < kTile; ++j) {
-                        x[j] = score_logit(x[j], a.score) - slope * (dist - (float)j);
-                        if (j >= valid) x[j] = -INFINITY;
+                for (int c = 0; c < kTile; c += 32) {
+                    float *const y = x[(c >> 5) & 1];
+                    tc_wait_ld();
+                    if (c + 32 < kTile) tmem_ld32(s_addr + c + 32, x[((c >> 5) & 1) ^ 1]);
+                    if (!as_is) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            y[j] = score_logit(y[j], a.score) - slope * (dist - (float)(c + j));
+                            if (c + j >= valid) y[j] = -INFINITY;
+                        }
+                        tmem_st32(s_addr + c, y);
                     }
-                    mult = 1.0f;
-                }
-                float top = x[0];
 #pragma unroll
-                for (int j = 1; j < kTile; ++j) top = fmaxf(top, x[j]);
-                top *= mult;
+                    for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], y[j]);
+                }
+                if (!as_is) tc_wait_st();
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mult;
                 if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
                     const float next = fmaxf(m, top);
                     const float w = m == next ? 1.0f : exp2_fast(m - next);
@@ -430,32 +472,45 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                     l *= w;
                     if (i > 0) {
                         // the products over earlier tiles are done: S of this tile came after them
-                        for (int c = 0; c < d; c += 32) {
-                            float o[32];
-                            tmem_ld32(o_addr + c, o);
+#pragma unroll 1
+                        for (int c = 0; c < d; c += 16) {
+                            float o[16];
+                            tmem_ld16(o_addr + c, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= w;
-                            tmem_st32(o_addr + c, o);
+                            for (int j = 0; j < 16; ++j) o[j] *= w;
+                            tmem_st16(o_addr + c, reinterpret_cast<const uint32_t *>(o));
                         }
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const Pair mult2(mult, mult), ref2(-ref, -ref);
+                Pair sum[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] = Pair(0.0f, 0.0f);
+                tmem_ld32(s_addr, x[0]);
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32) {
+                    const float *const y = x[(c >> 5) & 1];
+                    tc_wait_ld();
+                    if (c + 32 < kTile) tmem_ld32(s_addr + c + 32, x[((c >> 5) & 1) ^ 1]);
                     uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float p0 = exp2_fast(fmaf(x[c + j], mult, -ref));
-                        const float p1 = exp2_fast(fmaf(x[c + j + 1], mult, -ref));
-                        sum[j & 2] += p0;
-                        sum[(j & 2) + 1] += p1;
-                        p[j >> 1] = a.is_bf16 ? narrow2<__nv_bfloat16>(p0, p1) : narrow2<__half>(p0, p1);
+                        float p0, p1;
+                        fma2(Pair(y[j], y[j + 1]), mult2, ref2).split(p0, p1);
+                        p0 = exp2_fast(p0);
+                        p1 = exp2_fast(p1);
+                        sum[(j >> 1) & 3] = sum[(j >> 1) & 3] + Pair(p0, p1);
+                        p[j >> 1] = narrow2<T>(p0, p1);
                     }
-                    tmem_st16(s_addr + c / 2, p);
+                    tmem_st16(s_addr + c / 2, p);           // over columns that are read
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                {
+                    float s0, s1;
+                    ((sum[0] + sum[1]) + (sum[2] + sum[3])).split(s0, s1);
+                    l += s0 + s1;
+                }
                 tc_wait_st();
             }
             tc_before();
@@ -478,9 +533,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                     tc_wait_ld();
                     if (row < a.rows)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(a.pv.o + place * d + c + j) =
-                                make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 32; j += 8) store8(a.pv.o + place * d + c + j, o + j);
                 }
             }
             if (row < a.rows) a.pv.ml[place] = make_float2(m, l);
@@ -534,17 +587,29 @@ bool encode(CUtensorMap *map, const void *base, const PagedView &kv)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NB>
+template <typename T, int NB>
 cudaError_t launch_shape(const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
                          cudaStream_t stream)
 {
     using Shape = PrefixShape<NB>;
-    const cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<NB>,
+    const cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<T, NB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
     if (e != cudaSuccess) return e;
-    paged_prefix_kernel<NB><<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(kmap, vmap, a);
+    paged_prefix_kernel<T, NB><<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(kmap, vmap, a);
     note_launch();
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
+                        cudaStream_t stream)
+{
+    switch ((a.head_dim + 63) / 64) {
+    case 1: return launch_shape<T, 1>(kmap, vmap, a, ctas, stream);
+    case 2: return launch_shape<T, 2>(kmap, vmap, a, ctas, stream);
+    case 3: return launch_shape<T, 3>(kmap, vmap, a, ctas, stream);
+    default: return launch_shape<T, 4>(kmap, vmap, a, ctas, stream);
+    }
 }
 
 }  // namespace
@@ -579,7 +644,6 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.n_pages = kv.n_pages;
     a.page_shift = kv.page_shift;
     a.head_dim = kv.head_dim;
-    a.is_bf16 = kv.dtype == FATHOM_BF16;
     a.prefix_len = prefix_len;
     a.rows = p.rows;
     a.n_tiles = p.n_tiles;
@@ -589,12 +653,8 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.parts = p.parts;
     a.status = device_status_ptr();
     const int ctas = p.row_groups * kv.n_kv_heads * p.splits;
-    switch ((kv.head_dim + 63) / 64) {
-    case 1: return launch_shape<1>(kmap, vmap, a, ctas, stream);
-    case 2: return launch_shape<2>(kmap, vmap, a, ctas, stream);
-    case 3: return launch_shape<3>(kmap, vmap, a, ctas, stream);
-    default: return launch_shape<4>(kmap, vmap, a, ctas, stream);
-    }
+    return kv.dtype == FATHOM_BF16 ? launch_type<__nv_bfloat16>(kmap, vmap, a, ctas, stream)
+                                   : launch_type<__half>(kmap, vmap, a, ctas, stream);
 }
 
 }  // namespace fathom

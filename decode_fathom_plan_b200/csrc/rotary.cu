@@ -109,32 +109,6 @@ __device__ __forceinline__ void store_chunk(void *base, long long off, int dtype
         static_cast<__half *>(base)[off] = __float2half_rn(x[0]);
 }
 
-// Two float32 operations in one instruction.
-struct Pair {
-    unsigned long long v;
-    __device__ __forceinline__ Pair() {}
-    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ void split(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ Pair operator*(Pair a, Pair b)
-{
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair operator-(Pair a, Pair b)
-{
-    Pair r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
-{
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 // Rotates pairs of channels (x[j], y[j]), or two of them at once.
 __device__ __forceinline__ void rotate(float &x, float &y, float c, float s)
 {
