@@ -10,7 +10,8 @@
 //   warp 0      copies K and V tiles by TMA, one box per page, through a ring
 //               of stages; a page past the prefix, or a bad one, becomes an
 //               out-of-range coordinate, which TMA fills with zeros;
-//   warp 1      issues the products (one thread);
+//   warp 1      issues the products;
+//   warp 2      allocates TMEM;
 //   warps 4-7   softmax of slot 0, thread = row: S from TMEM, running maximum
 //   warps 8-11  and sum in registers, P back to TMEM over S; slot 1 likewise.
 // Two slots keep the tensor cores busy while a slot's softmax runs.  With more
@@ -95,24 +96,38 @@ __device__ __forceinline__ unsigned long long global_ns()
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// Waits for the phase of the given parity; false once *stop is set or the
-// limit is over (which sets it).
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *stop)
-{
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try(bar, parity)) {
-        if (*stop) return false;
-        if (global_ns() - t0 > kWaitNs) {
-            *stop = 1;
-            return false;
-        }
-    }
-    return true;
-}
+// Waits for the phase of the given parity, the whole warp together; false once
+// *stop is set or the limit is over (which sets it).  Inlined: the warps that
+// issue products and copies make no calls.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *stop)
 {
-    if (mbar_try(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, stop);
+    bool ok = mbar_try(bar, parity);
+    if (!ok) {
+        const unsigned long long start = global_ns();
+        do {
+            ok = mbar_try(bar, parity);
+            if (!ok && (*stop || global_ns() - start > kWaitNs)) {
+                *stop = 1;
+                break;
+            }
+        } while (!ok);
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+// The same after a stop, for what is still under way; gives up after the limit.
+__device__ __forceinline__ void wait_anyway(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long start = global_ns();
+    while (!mbar_try(bar, parity) && global_ns() - start < kWaitNs) {
+    }
+    __syncwarp();
+}
+// One lane of a warp that is together; the same one every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c,
                                          int slot, int head, int page)
@@ -272,7 +287,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
+    // by a warp that does nothing else: after code for one of its lanes a warp need not be together
+    // again for an aligned instruction
+    if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&s_tmem)),
                      "n"(kTmemCols)
@@ -293,25 +310,31 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         bool ok = true, bad = false;
         auto load = [&](const CUtensorMap *map, int tile) {
             const int stage = issued % kStages;
-            ok = ok && mbar_wait(empty + 8 * stage, ((issued / kStages) & 1) ^ 1, stop);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = mbar_wait(empty + 8 * stage, ((issued / kStages) & 1) ^ 1, stop);
             if (!ok) return;
-            const uint32_t dst = ring + stage * kTileBytes, bar = full + 8 * stage;
-            if (lane == 0) mbar_expect(bar, kTileBytes);
-            __syncwarp();
-            for (int i = lane; i < boxes * NB; i += 32) {
-                const int cb = i / boxes, x = i - cb * boxes;
-                const int key = (t0 + tile) * kTile + x * box;
-                int page = a.n_pages;
-                if (key < a.prefix_len) {
-                    page = a.table[key >> shift];
-                    if (page < 0 || page >= a.n_pages) {
-                        bad = true;
-                        page = a.n_pages;
-                    }
+            // lane x: the page of box x
+            const int key0 = (t0 + tile) * kTile, key = key0 + lane * box;
+            int page = a.n_pages;
+            if (lane < boxes && key < a.prefix_len) {
+                page = a.table[key >> shift];
+                if (page < 0 || page >= a.n_pages) {
+                    bad = true;
+                    page = a.n_pages;
                 }
-                tma_load(dst + cb * kBlockBytes + x * box * 128, map, bar, cb * 64,
-                         key & ((1 << shift) - 1), h, page);
+            }
+            const uint32_t dst = ring + stage * kTileBytes, bar = full + 8 * stage;
+            const int slot0 = key0 & ((1 << shift) - 1);        // not 0 where a page holds several tiles
+            __syncwarp();
+            if (elect_one()) mbar_expect(bar, kTileBytes);
+            __syncwarp();
+            for (int x = 0; x < boxes; ++x) {
+                const int p = __shfl_sync(0xFFFFFFFFu, page, x);
+                if (elect_one()) {
+#pragma unroll
+                    for (int cb = 0; cb < NB; ++cb)
+                        tma_load(dst + cb * kBlockBytes + x * box * 128, map, bar, cb * 64, slot0, h, p);
+                }
+                __syncwarp();
             }
             ++issued;
         };
@@ -323,69 +346,67 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 if (i < n && walk.has(i, s)) load(&kmap, walk.tile(i, s));
             }
         if (bad) set_status(a.status, FATHOM_ERR_INVALID_ARG);
-        if (!ok) {                                              // let the copies land
-            const unsigned long long start = global_ns();
+        if (!ok)                                                // let the copies land
             for (int x = max(0, issued - kStages); x < issued; ++x)
-                while (!mbar_try(full + 8 * (x % kStages), (x / kStages) & 1) &&
-                       global_ns() - start < kWaitNs) {
-                }
-        }
+                wait_anyway(full + 8 * (x % kStages), (x / kStages) & 1);
     } else if (warp == 1) {
         // ---------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-            const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((128u >> 4) << 24);
-            const uint32_t idesc_qk = common | ((uint32_t)(kTile >> 3) << 17);
-            const uint32_t idesc_pv = common | (1u << 16) | ((uint32_t)(d >> 3) << 17);
-            int used = 0, k_stage = 0, v_stage = 0, k_use = 0, v_use = 0;
-            bool ok = mbar_wait(q_ready, 0, stop);
-            const int n = walk.iterations();
-            for (int i = 0; i <= n && ok; ++i)
-                for (int s = 0; s < kSlots && ok; ++s) {
-                    const bool take = !shared || s == 0, last = !shared || s == kSlots - 1;
-                    if (walk.has(i - 1, s)) {
-                        if (take) {
-                            v_use = used++;
-                            v_stage = v_use % kStages;
-                        }
-                        ok = mbar_wait(p_ready + 8 * s, (i - 1) & 1, stop) &&
-                             mbar_wait(full + 8 * v_stage, (v_use / kStages) & 1, stop);
-                        if (!ok) break;
-                        tc_after();
-                        const uint32_t v = ring + v_stage * kTileBytes;
-                        for (int k = 0; k < kTile / 16; ++k)
-                            umma_ts(tmem + o_col + s * d, tmem + s * kTile + k * 8,
-                                    umma_desc(v + k * 2048, kBlockBytes), idesc_pv, i > 1 || k > 0);
-                        if (last) umma_commit(empty + 8 * v_stage);
-                        if (!walk.has(i, s)) umma_commit(o_ready + 8 * s);
+        const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((128u >> 4) << 24);
+        const uint32_t idesc_qk = common | ((uint32_t)(kTile >> 3) << 17);
+        const uint32_t idesc_pv = common | (1u << 16) | ((uint32_t)(d >> 3) << 17);
+        int used = 0, k_use = 0, v_use = 0;
+        bool ok = mbar_wait(q_ready, 0, stop);
+        const int n = walk.iterations();
+        for (int i = 0; i <= n && ok; ++i)
+            for (int s = 0; s < kSlots && ok; ++s) {
+                const bool take = !shared || s == 0, last = !shared || s == kSlots - 1;
+                if (walk.has(i - 1, s)) {
+                    if (take) {
+                        v_use = used++;
+                        ok = mbar_wait(full + 8 * (v_use % kStages), (v_use / kStages) & 1, stop);
                     }
-                    if (i < n && walk.has(i, s)) {
-                        if (take) {
-                            k_use = used++;
-                            k_stage = k_use % kStages;
-                        }
-                        ok = mbar_wait(full + 8 * k_stage, (k_use / kStages) & 1, stop);
+                    ok = ok && mbar_wait(p_ready + 8 * s, (i - 1) & 1, stop);
+                    if (!ok) break;
+                    tc_after();
+                    const uint64_t v = umma_desc(ring + v_use % kStages * kTileBytes, kBlockBytes);
+                    const bool ends = !walk.has(i, s);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)    // 16 keys: 2048 bytes of V, 8 columns of P
+                            umma_ts(tmem + o_col + s * d, tmem + s * kTile + k * 8, v + k * (2048 >> 4), idesc_pv,
+                                    i > 1 || k > 0);
+                        if (last) umma_commit(empty + 8 * (v_use % kStages));
+                        if (ends) umma_commit(o_ready + 8 * s);
+                    }
+                    __syncwarp();
+                }
+                if (i < n && walk.has(i, s)) {
+                    if (take) {
+                        k_use = used++;
+                        ok = mbar_wait(full + 8 * (k_use % kStages), (k_use / kStages) & 1, stop);
                         if (!ok) break;
                         tc_after();
-                        const uint32_t kk = ring + k_stage * kTileBytes;
-                        const uint32_t qq = q_addr + (shared ? s * kTileBytes : 0);
-                        for (int k = 0; k < d / 16; ++k) {
-                            const uint32_t off = (k >> 2) * kBlockBytes + (k & 3) * 32;
-                            umma_ss(tmem + s * kTile, umma_desc(qq + off, 16), umma_desc(kk + off, 16),
-                                    idesc_qk, k > 0);
+                    }
+                    const uint64_t k_desc = umma_desc(ring + k_use % kStages * kTileBytes, 16);
+                    const uint64_t q_desc = umma_desc(q_addr + (shared ? s * kTileBytes : 0), 16);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < NB * 4; ++k) {      // 16 channels: 32 bytes of a 64-channel block
+                            const int off = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
+                            if (k < d / 16) umma_ss(tmem + s * kTile, q_desc + off, k_desc + off, idesc_qk, k > 0);
                         }
-                        if (last) umma_commit(empty + 8 * k_stage);
+                        if (last) umma_commit(empty + 8 * (k_use % kStages));
                         umma_commit(s_ready + 8 * s);
                     }
-                }
-            if (!ok) {                                          // let the products end
-                umma_commit(drained);
-                const unsigned long long start = global_ns();
-                while (!mbar_try(drained, 0) && global_ns() - start < kWaitNs) {
+                    __syncwarp();
                 }
             }
+        if (!ok) {                                              // let the products end
+            if (elect_one()) umma_commit(drained);
+            __syncwarp();
+            wait_anyway(drained, 0);
         }
-        __syncwarp();
     } else if (warp >= 4) {
         // ----------------------------------------------------- softmax
         const int s = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
@@ -433,7 +454,6 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         bool ok = true;
         for (int i = 0; i < count; ++i) {
             ok = mbar_wait(s_ready + 8 * s, i & 1, stop);
-            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_after();
             if (live) {
@@ -444,26 +464,36 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 const bool as_is = plain && valid >= kTile;
                 const float mult = as_is ? a.score.scale : 1.0f;
                 const float dist = (float)(seq_len - 1 - key0);
+                __syncwarp();
                 float x[2][32];
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tmem_ld32(s_addr, x[0]);
+                if (as_is) {
+                    tmem_ld32(s_addr, x[0]);
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
-                    float *const y = x[(c >> 5) & 1];
-                    tc_wait_ld();
-                    if (c + 32 < kTile) tmem_ld32(s_addr + c + 32, x[((c >> 5) & 1) ^ 1]);
-                    if (!as_is) {
+                    for (int c = 0; c < kTile; c += 32) {
+                        const float *const y = x[(c >> 5) & 1];
+                        tc_wait_ld();
+                        if (c + 32 < kTile) tmem_ld32(s_addr + c + 32, x[((c >> 5) & 1) ^ 1]);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], y[j]);
+                    }
+                } else {
+                    // no load is under way across the branches of a score
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 32) {
+                        float *const y = x[0];
+                        tmem_ld32(s_addr + c, y);
+                        tc_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             y[j] = score_logit(y[j], a.score) - slope * (dist - (float)(c + j));
                             if (c + j >= valid) y[j] = -INFINITY;
+                            tops[j & 3] = fmaxf(tops[j & 3], y[j]);
                         }
                         tmem_st32(s_addr + c, y);
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], y[j]);
+                    tc_wait_st();
                 }
-                if (!as_is) tc_wait_st();
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mult;
                 if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
                     const float next = fmaxf(m, top);
@@ -517,10 +547,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready + 8 * s);
         }
-        if (ok && count > 0) {
-            ok = mbar_wait(o_ready + 8 * s, 0, stop);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-        }
+        if (ok && count > 0) ok = mbar_wait(o_ready + 8 * s, 0, stop);
         if (ok && live) {
             tc_after();
             const int part = shared ? split : split * kSlots + s;
@@ -542,7 +569,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     tc_before();
     __syncthreads();
     if (threadIdx.x == 0 && s_stop) set_status(a.status, FATHOM_ERR_TIMEOUT);
-    if (warp == 0) {
+    if (warp == 2) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
     }
