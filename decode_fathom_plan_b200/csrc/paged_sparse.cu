@@ -9,8 +9,15 @@
 // bytes of the row, a warp has eight keys at once, a dot product costs two
 // shuffles, and the sums over V need none: each group of four lanes keeps its
 // own running maximum, sum and output, which are joined once at the end.
-// A query's list is split into runs of kRunKeys keys, one CTA each.
+// A query's list is split into runs, one CTA each.  Registers (the output and
+// the query: 48 of some 126 at d = 128) leave 16 warps of 4 KB in flight a
+// multiprocessor; a second step's rows on their way at 12 warps was slower.
+// Measured on B200: 512 rows of 1024 keys of 128 channels, lists of 16
+// sequences, 55 us (4.3 TB/s, 67% of a plain copy, of single 256-byte rows); 32 rows of
+// 2048 keys 11.8 us.
 #include <math.h>
+
+#include <algorithm>
 
 #include "paged.cuh"
 
@@ -19,7 +26,6 @@ namespace {
 
 constexpr int kSparseThreads = 128;
 constexpr int kSparseWarps = kSparseThreads / 32;
-constexpr int kRunKeys = 128;
 
 struct SparseArgs {
     PagedView kv;
@@ -27,7 +33,7 @@ struct SparseArgs {
     PartsView pv;
     ScoreArgs score;
     const int32_t *idx;
-    int k, direct;
+    int k, run_keys, direct;
     int *status;
 };
 
@@ -51,75 +57,91 @@ paged_sparse_kernel(const SparseArgs a)
     const T *V = static_cast<const T *>(a.kv.v) + h * a.kv.head_stride + 8 * t;
     const float slope = a.q.slopes ? a.q.slopes[head] * kLog2e : 0.0f;
 
+    // Offset of the listed key i, -1 where there is none.  A warp looks its keys up 32 at a time, a
+    // lane each, one group ahead of the rows: a list entry, its page and its row are three
+    // dependent loads.
+    const int i1 = min(a.k, (run + 1) * a.run_keys);
+    const auto entry = [&](int i) { return i < i1 ? idx[i] : -1; };
+    bool bad = false;
+    const auto look_up = [&](int key) -> long long {
+        if (key == -1) return -1;
+        int page = -1;
+        if (key >= 0 && key < n && (key >> shift) < a.kv.table_stride) page = table[key >> shift];
+        if (page >= 0 && page < a.kv.n_pages)
+            return page * a.kv.page_stride + (key & mask) * a.kv.slot_stride;
+        bad = true;
+        return -1;
+    };
+    int i0 = run * a.run_keys + warp * 32;
+    int key_next = entry(i0 + lane), key_then = entry(i0 + kSparseWarps * 32 + lane);
     uint4 qr[E];
     {
         const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + head * a.q.q_hs + 8 * t;
 #pragma unroll
         for (int j = 0; j < E; ++j) qr[j] = *reinterpret_cast<const uint4 *>(q + 32 * j);
     }
+    long long at_next = look_up(key_next);
     float m = -INFINITY, l = 0.0f, o[E][8];
 #pragma unroll
     for (int j = 0; j < E; ++j)
 #pragma unroll
         for (int x = 0; x < 8; ++x) o[j][x] = 0.0f;
-    bool bad = false;
 
-    const int i1 = min(a.k, (run + 1) * kRunKeys);
-    for (int i0 = run * kRunKeys + warp * 8; i0 < i1; i0 += kSparseWarps * 8) {
-        const int i = i0 + (lane >> 2);
-        const int key = i < i1 ? idx[i] : -1;
-        long long at = -1;
-        if (key != -1) {
-            int page = -1;
-            if (key >= 0 && key < n && (key >> shift) < a.kv.table_stride) page = table[key >> shift];
-            if (page >= 0 && page < a.kv.n_pages)
-                at = page * a.kv.page_stride + (key & mask) * a.kv.slot_stride;
-            else
-                bad = true;
-        }
-        uint4 kr[E], vr[E];
+    for (; i0 < i1; i0 += kSparseWarps * 32) {
+        const int key_of = key_next;
+        const long long at_of = at_next;
+        key_next = key_then;
+        key_then = entry(i0 + 2 * kSparseWarps * 32 + lane);
+        at_next = look_up(key_next);
+#pragma unroll 2
+        for (int it = 0; it < 4; ++it) {
+            const int from = it * 8 + (lane >> 2);
+            const int key = __shfl_sync(0xFFFFFFFFu, key_of, from);
+            const long long at = __shfl_sync(0xFFFFFFFFu, at_of, from);
+            uint4 kr[E], vr[E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            kr[j] = vr[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (at >= 0) {
-                kr[j] = __ldg(reinterpret_cast<const uint4 *>(K + at + 32 * j));
-                vr[j] = __ldg(reinterpret_cast<const uint4 *>(V + at + 32 * j));
+            for (int j = 0; j < E; ++j) {
+                kr[j] = vr[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (at >= 0) {
+                    kr[j] = __ldg(reinterpret_cast<const uint4 *>(K + at + 32 * j));
+                    vr[j] = __ldg(reinterpret_cast<const uint4 *>(V + at + 32 * j));
+                }
             }
-        }
-        float dot = 0.0f;
+            float dot = 0.0f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const uint32_t ku[4] = {kr[j].x, kr[j].y, kr[j].z, kr[j].w};
-            const uint32_t qu[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
+            for (int j = 0; j < E; ++j) {
+                const uint32_t ku[4] = {kr[j].x, kr[j].y, kr[j].z, kr[j].w};
+                const uint32_t qu[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float2 kf = widen2<T>(ku[x]), qf = widen2<T>(qu[x]);
-                dot = fmaf(kf.x, qf.x, fmaf(kf.y, qf.y, dot));
+                for (int x = 0; x < 4; ++x) {
+                    const float2 kf = widen2<T>(ku[x]), qf = widen2<T>(qu[x]);
+                    dot = fmaf(kf.x, qf.x, fmaf(kf.y, qf.y, dot));
+                }
             }
-        }
-        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
-        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
-        const float s = at >= 0 ? score_logit(dot, a.score) - slope * (float)(n - 1 - key) : -INFINITY;
-        if (__any_sync(0xFFFFFFFFu, s > m + kRescale)) {
-            const float next = fmaxf(m, s);
-            const float w = m == next ? 1.0f : exp2_fast(m - next);
-            m = next;
-            l *= w;
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 1);
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, 2);
+            const float s = at >= 0 ? score_logit(dot, a.score) - slope * (float)(n - 1 - key) : -INFINITY;
+            if (__any_sync(0xFFFFFFFFu, s > m + kRescale)) {
+                const float next = fmaxf(m, s);
+                const float w = m == next ? 1.0f : exp2_fast(m - next);
+                m = next;
+                l *= w;
 #pragma unroll
-            for (int j = 0; j < E; ++j)
+                for (int j = 0; j < E; ++j)
 #pragma unroll
-                for (int x = 0; x < 8; ++x) o[j][x] *= w;
-        }
-        const float p = exp2_fast(s - (m == -INFINITY ? 0.0f : m));
-        l += p;
+                    for (int x = 0; x < 8; ++x) o[j][x] *= w;
+            }
+            const float p = exp2_fast(s - (m == -INFINITY ? 0.0f : m));
+            l += p;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const uint32_t vu[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
+            for (int j = 0; j < E; ++j) {
+                const uint32_t vu[4] = {vr[j].x, vr[j].y, vr[j].z, vr[j].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float2 vf = widen2<T>(vu[x]);
-                o[j][2 * x] = fmaf(p, vf.x, o[j][2 * x]);
-                o[j][2 * x + 1] = fmaf(p, vf.y, o[j][2 * x + 1]);
+                for (int x = 0; x < 4; ++x) {
+                    const float2 vf = widen2<T>(vu[x]);
+                    o[j][2 * x] = fmaf(p, vf.x, o[j][2 * x]);
+                    o[j][2 * x + 1] = fmaf(p, vf.y, o[j][2 * x + 1]);
+                }
             }
         }
     }
@@ -196,27 +218,37 @@ void launch_sparse(const SparseArgs &a, dim3 grid, cudaStream_t stream)
     }
 }
 
-int sparse_runs(int k) { return (k - 1) / kRunKeys + 1; }
+// Keys of a CTA: a group of 32 for each warp, or several (whose look-ups then overlap) where
+// there are rows enough.
+int sparse_run_keys(int n_rows, int k)
+{
+    const long long groups = (long long)n_rows * k / (148 * 8);
+    return (int)std::min<long long>(std::max<long long>(groups / 128 * 128, 128), 512);
+}
+int sparse_runs(int n_rows, int k) { return (k - 1) / sparse_run_keys(n_rows, k) + 1; }
 
 }  // namespace
 
 size_t paged_sparse_bytes(int n_rows, int head_dim, int k)
 {
-    return sparse_runs(k) == 1 ? 0 : parts_bytes((size_t)n_rows * sparse_runs(k), head_dim);
+    const int runs = sparse_runs(n_rows, k);
+    return runs == 1 ? 0 : parts_bytes((size_t)n_rows * runs, head_dim);
 }
 
 cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const int32_t *idx, int k,
                                 void *ws, cudaStream_t stream)
 {
-    const int n_heads = kv.n_kv_heads * q.group, runs = sparse_runs(k);
+    const int n_heads = kv.n_kv_heads * q.group, rows = q.n_seqs * n_heads;
+    const int runs = sparse_runs(rows, k);
     SparseArgs a{};
     a.kv = kv;
     a.q = q;
     a.score = score_args(q.softmax_scale, q.softcap);
     a.idx = idx;
     a.k = k;
+    a.run_keys = sparse_run_keys(rows, k);
     a.direct = runs == 1;
-    if (!a.direct) a.pv = parts_carve(ws, (size_t)q.n_seqs * n_heads * runs, kv.head_dim);
+    if (!a.direct) a.pv = parts_carve(ws, (size_t)rows * runs, kv.head_dim);
     a.status = device_status_ptr();
     const dim3 grid(runs, n_heads, q.n_seqs);
     if (kv.dtype == FATHOM_BF16)
