@@ -43,14 +43,17 @@ bool rotary_ok(const fathom_rotary *r, int head_dim)
            (r->interleaved == 0 || r->interleaved == 1) && isfinite(r->magnitude);
 }
 
+// A stride over n > 1 rows that are read or written 16 bytes at a time.
+bool stride_ok(int64_t stride, int n) { return n == 1 || (stride > 0 && stride % 8 == 0); }
+
 bool cache_ok(const fathom_kv_cache *c)
 {
     return c && c->n_pages >= 1 && c->page_size >= 8 && c->page_size <= 1024 &&
            (c->page_size & (c->page_size - 1)) == 0 && c->n_kv_heads >= 1 &&
            c->n_kv_heads <= kMaxHeads && head_dim_ok(c->head_dim) &&
-           (c->dtype == FATHOM_BF16 || c->dtype == FATHOM_F16) && c->page_stride >= 0 &&
-           c->head_stride >= 0 && c->token_stride >= 0 && c->page_stride % 8 == 0 &&
-           c->head_stride % 8 == 0 && c->token_stride % 8 == 0;
+           (c->dtype == FATHOM_BF16 || c->dtype == FATHOM_F16) &&
+           stride_ok(c->page_stride, c->n_pages) && stride_ok(c->head_stride, c->n_kv_heads) &&
+           stride_ok(c->token_stride, c->page_size);
 }
 
 int log2_of(int x)
@@ -107,7 +110,9 @@ int query_group(const fathom_kv_cache *c, const fathom_rows *q, const fathom_row
                 int32_t n_seqs, float scale, float softcap)
 {
     if (!rows_ok(q, n_seqs) || !rows_ok(out, n_seqs) || q->dtype != c->dtype || out->dtype != c->dtype) return 0;
-    if (!rows_vector(q) || !rows_vector(out) || q->n_heads != out->n_heads) return 0;
+    if (!aligned16(q->data) || !aligned16(out->data) || q->n_heads != out->n_heads) return 0;
+    for (const fathom_rows *r : {q, out})
+        if (!stride_ok(r->token_stride, n_seqs) || !stride_ok(r->head_stride, r->n_heads)) return 0;
     if (q->n_heads % c->n_kv_heads || q->n_heads / c->n_kv_heads > kMaxGroup) return 0;
     if (n_seqs < 1 || n_seqs > kMaxSequences || (long long)n_seqs * q->n_heads >= (1ll << 31)) return 0;
     if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return 0;

@@ -217,10 +217,10 @@ struct MergeArgs {
 cudaError_t launch_merge_parts(const MergeArgs &a, int dtype, cudaStream_t stream);
 
 // ---- paged_prefix.cu
-// How the products over a shared prefix are split: rows of a KV head, CTAs of
-// up to two blocks of 128 of them, runs of key tiles, places per row.
+// How the products over a shared prefix are split: sequences of a block of up
+// to 128 rows, CTAs of one or two blocks, runs of key tiles, places per row.
 struct PrefixPlan {
-    int rows, two_blocks, row_groups, n_tiles, splits, parts;
+    int slot_seqs, two_blocks, row_groups, n_tiles, splits, parts;
 };
 PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int prefix_len);
 // Writes the first p.parts places of every row.

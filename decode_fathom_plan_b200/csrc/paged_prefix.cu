@@ -38,8 +38,10 @@ namespace {
 
 constexpr int kRows = 128;                       // rows of a slot
 constexpr int kTile = 128;                       // keys of a tile
+constexpr int kStep = 64;                        // keys of a product
 constexpr int kBlockBytes = kTile * 128;         // 128 rows of 64 channels (128 bytes, swizzled)
 constexpr unsigned long long kWaitNs = 500000000ull;
+constexpr unsigned long long kSettleNs = 1000000ull;   // for copies under way after a stop
 constexpr int kTmemCols = 512;
 
 template <int NB>
@@ -57,7 +59,7 @@ struct PrefixArgs {
     ScoreArgs score;
     const int32_t *table;                        // the first row of the page table
     int n_heads, n_pages, page_shift, head_dim;
-    int prefix_len, rows, n_tiles, splits, row_groups, two_blocks, parts;
+    int prefix_len, seqs, slot_seqs, n_tiles, splits, row_groups, two_blocks, parts;
     int *status;
 };
 
@@ -128,6 +130,15 @@ __device__ __forceinline__ bool elect_one()
     uint32_t one;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
     return one != 0;
+}
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c, int head,
+                                          int seq)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(c), "r"(head), "r"(seq), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c,
                                          int slot, int head, int page)
@@ -228,37 +239,55 @@ __device__ __forceinline__ void store8(float *p, const float *x)
                  : "memory");
 }
 
-// Walks the steps (iteration, slot) of a CTA in the order in which their
-// tiles are consumed; the copying and the issuing warp follow the same walk.
-// At each step comes first V of the slot's previous tile, then K of its next.
+// Which tiles the slots of a CTA take, each in two steps of kStep keys.  The
+// warps that copy and the one that issues products walk the same order: K of
+// every slot's first tile, then at each even step j, slot by slot, V of the
+// tile of step j and K of the tile of step j + 2.
 struct Walk {
     int tiles;        // of this CTA
     int slots;
-    bool shared;      // the slots take the same tiles (else tile 2i + s)
-    __device__ int iterations() const { return shared ? tiles : (tiles + slots - 1) / slots; }
+    bool shared;      // the slots take the same tiles (else tile slots*i + s)
     __device__ int tile(int i, int s) const { return shared ? i : i * slots + s; }
-    __device__ bool has(int i, int s) const { return i >= 0 && tile(i, s) < tiles; }
-    __device__ int count(int s) const { return shared ? tiles : (tiles - s + slots - 1) / slots; }
+    __device__ int steps(int s) const { return 2 * (shared ? tiles : (tiles - s + slots - 1) / slots); }
+    __device__ int takers() const { return shared ? 1 : slots; }
+};
+// Place in the ring of stages.
+template <int STAGES>
+struct Place {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 // grid: (row group, KV head) fastest, then the run of tiles
 template <typename T, int NB>
 __global__ void __launch_bounds__(PrefixShape<NB>::kThreads, 1)
-paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                    const PrefixArgs a)
+paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, const PrefixArgs a)
 {
     using Shape = PrefixShape<NB>;
     constexpr int kSlots = Shape::kSlots, kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
+    constexpr int kThreads = Shape::kThreads;
     let_next_kernel_start();
     extern __shared__ unsigned char s_raw[];
-    __shared__ alignas(8) uint64_t s_bar[2 * kStages + 3 * kSlots + 2];
+    // Of slot s and step j: S, P and the product with V each at 2*s + (j & 1) of their barriers,
+    // phase j / 2.  With one barrier for every step a waiter could be two phases off, which a
+    // phase's parity does not show.
+    constexpr int kFull = 0, kEmpty = kStages, kScores = 2 * kStages, kProbs = kScores + 2 * kSlots,
+                  kDone = kProbs + 2 * kSlots, kQueries = kDone + 2 * kSlots, kDrained = kQueries + 1,
+                  kBarriers = kDrained + 1;
+    __shared__ alignas(8) uint64_t s_bar[kBarriers];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
-    const uint32_t q_addr = base, ring = base + kSlots * kTileBytes;
-    const uint32_t full = smem_u32(s_bar), empty = full + 8 * kStages, s_ready = empty + 8 * kStages,
-                   p_ready = s_ready + 8 * kSlots, o_ready = p_ready + 8 * kSlots,
-                   q_ready = o_ready + 8 * kSlots, drained = q_ready + 8;
+    const uint32_t q_addr = base, ring = base + kSlots * kTileBytes, bars = smem_u32(s_bar);
+    const auto bar = [&](int i) { return bars + 8 * i; };
 
     const int per = gridDim.x / a.splits;                       // row groups * KV heads
     const int split = blockIdx.x / per, unit = blockIdx.x - split * per;
@@ -267,248 +296,249 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     const int t1 = (int)((long long)(split + 1) * a.n_tiles / a.splits);
     const bool shared = a.two_blocks || kSlots == 1;
     const Walk walk{t1 - t0, kSlots, shared};
-    const int row0 = group * kRows * (shared ? kSlots : 1);     // of slot 0
+    const int seq0 = group * a.slot_seqs * (shared ? kSlots : 1);   // of slot 0
     const int d = a.head_dim, G = a.q.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *stop = &s_stop;
-
-    if (threadIdx.x == 0) {
-        s_stop = 0;
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, 1);
-        }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(s_ready + 8 * s, 1);
-            mbar_init(p_ready + 8 * s, 4);
-            mbar_init(o_ready + 8 * s, 1);
-        }
-        mbar_init(q_ready, 4 * kSlots);
-        mbar_init(drained, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    // by a warp that does nothing else: after code for one of its lanes a warp need not be together
-    // again for an aligned instruction
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&s_tmem)),
-                     "n"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_before();
-    __syncthreads();
-    tc_after();
-    const uint32_t tmem = s_tmem;
     const uint32_t o_col = kSlots * kTile;                      // O of slot s at o_col + s*d
 
     if (warp == 0) {
-        // ------------------------------------------------------ copies
+        for (int i = lane; i < kBarriers; i += 32) mbar_init(bar(i), i >= kProbs && i < kDone ? 4 : 1);
+        if (lane == 0) s_stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------ copies: K (and Q) or V
+        const bool keys = warp == 0;
+        const CUtensorMap *map = keys ? &kmap : &vmap;
         const int shift = a.page_shift, box = min(1 << shift, kTile);
         const int boxes = kTile / box;                          // per 64-channel block
-        int issued = 0;
-        bool ok = true, bad = false;
-        auto load = [&](const CUtensorMap *map, int tile) {
-            const int stage = issued % kStages;
-            ok = mbar_wait(empty + 8 * stage, ((issued / kStages) & 1) ^ 1, stop);
-            if (!ok) return;
-            // lane x: the page of box x
-            const int key0 = (t0 + tile) * kTile, key = key0 + lane * box;
-            int page = a.n_pages;
-            if (lane < boxes && key < a.prefix_len) {
-                page = a.table[key >> shift];
-                if (page < 0 || page >= a.n_pages) {
-                    bad = true;
-                    page = a.n_pages;
-                }
-            }
-            const uint32_t dst = ring + stage * kTileBytes, bar = full + 8 * stage;
-            const int slot0 = key0 & ((1 << shift) - 1);        // not 0 where a page holds several tiles
+        // lane x: the page of box x of a tile, looked up a tile ahead
+        const auto page_of = [&](int tile) {
+            const int key = (t0 + tile) * kTile + lane * box;
+            return lane < boxes && key < a.prefix_len ? a.table[key >> shift] : a.n_pages;
+        };
+        int page = page_of(0);
+        if (keys) {
             __syncwarp();
-            if (elect_one()) mbar_expect(bar, kTileBytes);
-            __syncwarp();
-            for (int x = 0; x < boxes; ++x) {
-                const int p = __shfl_sync(0xFFFFFFFFu, page, x);
-                if (elect_one()) {
+            // the others wait for this, and for TMEM; the first copies of Q and K do not
+            asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory");
+            const int slots = shared ? kSlots : 1, box_bytes = a.slot_seqs * G * 128;
+            if (elect_one()) {
+                mbar_expect(bar(kQueries), slots * NB * box_bytes);
+                for (int s = 0; s < slots; ++s)
 #pragma unroll
                     for (int cb = 0; cb < NB; ++cb)
-                        tma_load(dst + cb * kBlockBytes + x * box * 128, map, bar, cb * 64, slot0, h, p);
+                        tma_load3(q_addr + s * kTileBytes + cb * kBlockBytes, &qmap, bar(kQueries), cb * 64, h * G,
+                                  seq0 + s * a.slot_seqs);
+            }
+            __syncwarp();
+        } else {
+            asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
+        }
+        Place<kStages> at;
+        int issued = 0;
+        bool ok = true, bad = false;
+        const auto load = [&](bool mine, int tile) {
+            if (ok && mine) ok = mbar_wait(bar(kEmpty + at.stage), at.phase ^ 1, stop);
+            if (ok && mine) {
+                int p = page;
+                if (p < 0 || p > a.n_pages || (p == a.n_pages && lane < boxes &&
+                                               (t0 + tile) * kTile + lane * box < a.prefix_len)) {
+                    bad = true;
+                    p = a.n_pages;
+                }
+                page = page_of(tile + 1);
+                int pages[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) pages[x] = __shfl_sync(0xFFFFFFFFu, p, x);
+                const uint32_t dst = ring + at.stage * kTileBytes, full = bar(kFull + at.stage);
+                const int slot0 = ((t0 + tile) * kTile) & ((1 << shift) - 1);   // a page may hold several tiles
+                if (elect_one()) {
+                    mbar_expect(full, kTileBytes);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        if (x < boxes)
+#pragma unroll
+                            for (int cb = 0; cb < NB; ++cb)
+                                tma_load(dst + cb * kBlockBytes + x * box * 128, map, full, cb * 64, slot0, h,
+                                         pages[x]);
+                }
+                __syncwarp();
+                ++issued;
+            }
+            at.next();
+        };
+        const int takers = walk.takers(), n = walk.steps(0);
+        for (int s = 0; s < takers; ++s)
+            if (walk.steps(s) > 0) load(keys, walk.tile(0, s));
+        for (int j = 0; j < n && ok; j += 2)
+            for (int s = 0; s < takers; ++s) {
+                if (j < walk.steps(s)) load(!keys, walk.tile(j >> 1, s));
+                if (j + 2 < walk.steps(s)) load(keys, walk.tile((j + 2) >> 1, s));
+            }
+        if (bad) set_status(a.status, FATHOM_ERR_INVALID_ARG);
+        if (!ok && issued) {                                    // let the copies land
+            if (keys) wait_anyway(bar(kQueries), 0);
+            const unsigned long long start = global_ns();
+            while (global_ns() - start < kSettleNs) {
+            }
+            __syncwarp();
+        }
+    } else if (warp < 4) {
+        // by a warp that does nothing else: after code for one of its lanes a warp need not be
+        // together again for an aligned instruction
+        if (warp == 2) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&s_tmem)),
+                         "n"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+            tc_before();
+        }
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
+        if (warp == 1) {
+            // ------------------------------------------------ products
+            tc_after();
+            const uint32_t tmem = s_tmem;
+            const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+            const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((128u >> 4) << 24);
+            const uint32_t idesc_qk = common | ((uint32_t)(kStep >> 3) << 17);
+            const uint32_t idesc_pv = common | (1u << 16) | ((uint32_t)(d >> 3) << 17);
+            const uint64_t k_ring = umma_desc(ring, 16), v_ring = umma_desc(ring, kBlockBytes);
+            const uint64_t q_first = umma_desc(q_addr, 16);
+            constexpr int kStageStep = kTileBytes >> 4, kHalfStep = (kStep * 128) >> 4;
+            Place<kStages> at;
+            int k_stage[kSlots] = {}, v_stage[kSlots] = {};
+            int steps[kSlots];
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) steps[s] = walk.steps(s);
+            bool ok = mbar_wait(bar(kQueries), 0, stop);
+            const auto take = [&](int &stage) {
+                stage = at.stage;
+                ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop);
+                at.next();
+            };
+            // S = Q K^T of step j, by one lane
+            const auto scores = [&](int j, int s, int stage) {
+                const uint64_t k_desc = k_ring + stage * kStageStep + (j & 1) * kHalfStep;
+                const uint64_t q_desc = q_first + (shared ? s * kStageStep : 0);
+#pragma unroll
+                for (int k = 0; k < NB * 4; ++k) {              // 16 channels: 32 bytes of a 64-channel block
+                    const int off = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
+                    if (k < d / 16)
+                        umma_ss(tmem + s * kTile + (j & 1) * kStep, q_desc + off, k_desc + off, idesc_qk, k > 0);
+                }
+                umma_commit(bar(kScores + 2 * s + (j & 1)));
+            };
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                if (steps[s] == 0) continue;
+                if (!shared || s == 0) take(k_stage[s]);
+                const int k = shared ? k_stage[0] : k_stage[s];
+                tc_after();
+                if (ok && elect_one()) {
+                    scores(0, s, k);
+                    scores(1, s, k);
+                    if (!shared || s == kSlots - 1) umma_commit(bar(kEmpty + k));
                 }
                 __syncwarp();
             }
-            ++issued;
-        };
-        const int n = walk.iterations();
-        for (int i = 0; i <= n && ok; ++i)
-            for (int s = 0; s < kSlots && ok; ++s) {
-                if (shared && s > 0) continue;
-                if (walk.has(i - 1, s)) load(&vmap, walk.tile(i - 1, s));
-                if (i < n && walk.has(i, s)) load(&kmap, walk.tile(i, s));
-            }
-        if (bad) set_status(a.status, FATHOM_ERR_INVALID_ARG);
-        if (!ok)                                                // let the copies land
-            for (int x = max(0, issued - kStages); x < issued; ++x)
-                wait_anyway(full + 8 * (x % kStages), (x / kStages) & 1);
-    } else if (warp == 1) {
-        // ---------------------------------------------------- products
-        const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-        const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((128u >> 4) << 24);
-        const uint32_t idesc_qk = common | ((uint32_t)(kTile >> 3) << 17);
-        const uint32_t idesc_pv = common | (1u << 16) | ((uint32_t)(d >> 3) << 17);
-        int used = 0, k_use = 0, v_use = 0;
-        bool ok = mbar_wait(q_ready, 0, stop);
-        const int n = walk.iterations();
-        for (int i = 0; i <= n && ok; ++i)
-            for (int s = 0; s < kSlots && ok; ++s) {
-                const bool take = !shared || s == 0, last = !shared || s == kSlots - 1;
-                if (walk.has(i - 1, s)) {
-                    if (take) {
-                        v_use = used++;
-                        ok = mbar_wait(full + 8 * (v_use % kStages), (v_use / kStages) & 1, stop);
+            for (int j = 0; j < steps[0] && ok; ++j)
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    if (j >= steps[s]) continue;
+                    const bool more = j + 2 < steps[s];
+                    if (!(j & 1) && (!shared || s == 0)) {
+                        take(v_stage[s]);
+                        if (more) take(k_stage[s]);
                     }
-                    ok = ok && mbar_wait(p_ready + 8 * s, (i - 1) & 1, stop);
-                    if (!ok) break;
+                    ok = ok && mbar_wait(bar(kProbs + 2 * s + (j & 1)), (j >> 1) & 1, stop);
                     tc_after();
-                    const uint64_t v = umma_desc(ring + v_use % kStages * kTileBytes, kBlockBytes);
-                    const bool ends = !walk.has(i, s);
-                    if (elect_one()) {
+                    const int v = shared ? v_stage[0] : v_stage[s], k = shared ? k_stage[0] : k_stage[s];
+                    const bool free = (j & 1) && (!shared || s == kSlots - 1);
+                    const uint64_t v_desc = v_ring + v * kStageStep + (j & 1) * kHalfStep;
+                    if (ok && elect_one()) {
+                        // O += P V of step j; then S of step j + 2 goes where P was
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)    // 16 keys: 2048 bytes of V, 8 columns of P
-                            umma_ts(tmem + o_col + s * d, tmem + s * kTile + k * 8, v + k * (2048 >> 4), idesc_pv,
-                                    i > 1 || k > 0);
-                        if (last) umma_commit(empty + 8 * (v_use % kStages));
-                        if (ends) umma_commit(o_ready + 8 * s);
-                    }
-                    __syncwarp();
-                }
-                if (i < n && walk.has(i, s)) {
-                    if (take) {
-                        k_use = used++;
-                        ok = mbar_wait(full + 8 * (k_use % kStages), (k_use / kStages) & 1, stop);
-                        if (!ok) break;
-                        tc_after();
-                    }
-                    const uint64_t k_desc = umma_desc(ring + k_use % kStages * kTileBytes, 16);
-                    const uint64_t q_desc = umma_desc(q_addr + (shared ? s * kTileBytes : 0), 16);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < NB * 4; ++k) {      // 16 channels: 32 bytes of a 64-channel block
-                            const int off = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
-                            if (k < d / 16) umma_ss(tmem + s * kTile, q_desc + off, k_desc + off, idesc_qk, k > 0);
+                        for (int x = 0; x < kStep / 16; ++x)    // 16 keys: 2048 bytes of V, 8 columns of P
+                            umma_ts(tmem + o_col + s * d, tmem + s * kTile + (j & 1) * kStep + x * 8,
+                                    v_desc + x * (2048 >> 4), idesc_pv, j > 0 || x > 0);
+                        umma_commit(bar(kDone + 2 * s + (j & 1)));
+                        if (free) umma_commit(bar(kEmpty + v));
+                        if (more) {
+                            scores(j + 2, s, k);
+                            if (free) umma_commit(bar(kEmpty + k));
                         }
-                        if (last) umma_commit(empty + 8 * (k_use % kStages));
-                        umma_commit(s_ready + 8 * s);
                     }
                     __syncwarp();
                 }
+            if (!ok) {                                          // let the products end
+                if (elect_one()) umma_commit(bar(kDrained));
+                __syncwarp();
+                wait_anyway(bar(kDrained), 0);
             }
-        if (!ok) {                                              // let the products end
-            if (elect_one()) umma_commit(drained);
-            __syncwarp();
-            wait_anyway(drained, 0);
         }
-    } else if (warp >= 4) {
+    } else {
         // ----------------------------------------------------- softmax
         const int s = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-        const int row = row0 + (shared ? s * kRows : 0) + r;
-        const bool live = row - lane < a.rows;                  // of the warp: any row at all
-        const int b = min(row, a.rows - 1) / G, head = h * G + min(row, a.rows - 1) - b * G;
-        {
-            // the warp's 32 rows of Q into their swizzled tile; slots with the same rows take turns
-            const long long mine = b * a.q.q_ts + head * a.q.q_hs;
-            const uint16_t *q = static_cast<const uint16_t *>(a.q.q);
-            const uint32_t to = q_addr + (shared ? s * kTileBytes : 0);
-            constexpr int kChunks = NB * 8, kBatch = 8;
-            const int first = shared ? 0 : s, step = shared ? 1 : kSlots;
-            for (int i0 = first; i0 < kChunks; i0 += kBatch * step) {
-                uint4 u[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + k * step, x = (i * 32 + lane) / kChunks, c = (i * 32 + lane) - x * kChunks;
-                    const long long off = __shfl_sync(0xFFFFFFFFu, mine, x & 31);
-                    u[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (i < kChunks && c * 8 < d && live) u[k] = *reinterpret_cast<const uint4 *>(q + off + 8 * c);
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int i = i0 + k * step, x = (i * 32 + lane) / kChunks, c = (i * 32 + lane) - x * kChunks;
-                    const int at = (warp & 3) * 32 + x;
-                    if (i < kChunks)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         to + (c >> 3) * kBlockBytes + at * 128 + (((c & 7) ^ (at & 7)) << 4)),
-                                     "r"(u[k].x), "r"(u[k].y), "r"(u[k].z), "r"(u[k].w)
-                                     : "memory");
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready);
-        }
+        const int seq = seq0 + (shared ? s * a.slot_seqs : 0) + r / G;
+        const bool mine = r < a.slot_seqs * G && seq < a.seqs;
+        const bool live = __any_sync(0xFFFFFFFFu, mine);
+        const int b = mine ? seq : 0, head = h * G + r % G;
         const int seq_len = a.q.seq_lens[b];
         const float slope = a.q.slopes ? a.q.slopes[head] * kLog2e : 0.0f;
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
+        tc_after();
         const bool plain = a.score.cap == 0.0f && !a.q.slopes && a.score.scale > 0.0f;
-        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_addr = lane_addr + s * kTile, o_addr = lane_addr + o_col + s * d;
-        const int count = walk.count(s);
+        const uint32_t lane_addr = s_tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t o_addr = lane_addr + o_col + s * d;
+        const int steps = walk.steps(s);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
-        for (int i = 0; i < count; ++i) {
-            ok = mbar_wait(s_ready + 8 * s, i & 1, stop);
+        for (int j = 0; j < steps; ++j) {
+            const int which = 2 * s + (j & 1);
+            const uint32_t s_addr = lane_addr + s * kTile + (j & 1) * kStep;
+            ok = mbar_wait(bar(kScores + which), (j >> 1) & 1, stop);
             if (!ok) break;
             tc_after();
             if (live) {
-                // Twice over the row, 32 columns at a time and the next ones on their way: the
-                // maximum, then the probabilities.  (A row held in registers would be 128 of them.)
-                const int key0 = (t0 + walk.tile(i, s)) * kTile;
-                const int valid = a.prefix_len - key0;          // keys of this tile
-                const bool as_is = plain && valid >= kTile;
-                const float mult = as_is ? a.score.scale : 1.0f;
-                const float dist = (float)(seq_len - 1 - key0);
-                __syncwarp();
-                float x[2][32];
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (as_is) {
-                    tmem_ld32(s_addr, x[0]);
+                const int key0 = (t0 + walk.tile(j >> 1, s)) * kTile + (j & 1) * kStep;
+                const int valid = a.prefix_len - key0;          // keys of this step
+                float x[kStep];
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 32) {
-                        const float *const y = x[(c >> 5) & 1];
-                        tc_wait_ld();
-                        if (c + 32 < kTile) tmem_ld32(s_addr + c + 32, x[((c >> 5) & 1) ^ 1]);
+                for (int c = 0; c < kStep; c += 32) tmem_ld32(s_addr + c, x + c);
+                tc_wait_ld();
+                float mult = a.score.scale;
+                if (!plain || valid < kStep) {
+                    const float dist = (float)(seq_len - 1 - key0);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], y[j]);
+                    for (int k = 0; k < kStep; ++k) {
+                        x[k] = score_logit(x[k], a.score) - slope * (dist - (float)k);
+                        if (k >= valid) x[k] = -INFINITY;
                     }
-                } else {
-                    // no load is under way across the branches of a score
-#pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32) {
-                        float *const y = x[0];
-                        tmem_ld32(s_addr + c, y);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            y[j] = score_logit(y[j], a.score) - slope * (dist - (float)(c + j));
-                            if (c + j >= valid) y[j] = -INFINITY;
-                            tops[j & 3] = fmaxf(tops[j & 3], y[j]);
-                        }
-                        tmem_st32(s_addr + c, y);
-                    }
-                    tc_wait_st();
+                    mult = 1.0f;
                 }
+                float tops[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int k = 4; k < kStep; ++k) tops[k & 3] = fmaxf(tops[k & 3], x[k]);
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mult;
                 if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
                     const float next = fmaxf(m, top);
                     const float w = m == next ? 1.0f : exp2_fast(m - next);
                     m = next;
                     l *= w;
-                    if (i > 0) {
-                        // the products over earlier tiles are done: S of this tile came after them
+                    if (j > 0) {
+                        ok = mbar_wait(bar(kDone + 2 * s + ((j - 1) & 1)), ((j - 1) >> 1) & 1, stop);
+                        if (!ok) break;
+                        tc_after();
 #pragma unroll 1
                         for (int c = 0; c < d; c += 16) {
                             float o[16];
                             tmem_ld16(o_addr + c, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] *= w;
+                            for (int k = 0; k < 16; ++k) o[k] *= w;
                             tmem_st16(o_addr + c, reinterpret_cast<const uint32_t *>(o));
                         }
                     }
@@ -518,24 +548,17 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 Pair sum[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sum[k] = Pair(0.0f, 0.0f);
-                tmem_ld32(s_addr, x[0]);
+                uint32_t p[kStep / 2];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) {
-                    const float *const y = x[(c >> 5) & 1];
-                    tc_wait_ld();
-                    if (c + 32 < kTile) tmem_ld32(s_addr + c + 32, x[((c >> 5) & 1) ^ 1]);
-                    uint32_t p[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float p0, p1;
-                        fma2(Pair(y[j], y[j + 1]), mult2, ref2).split(p0, p1);
-                        p0 = exp2_fast(p0);
-                        p1 = exp2_fast(p1);
-                        sum[(j >> 1) & 3] = sum[(j >> 1) & 3] + Pair(p0, p1);
-                        p[j >> 1] = narrow2<T>(p0, p1);
-                    }
-                    tmem_st16(s_addr + c / 2, p);           // over columns that are read
+                for (int k = 0; k < kStep; k += 2) {
+                    float p0, p1;
+                    fma2(Pair(x[k], x[k + 1]), mult2, ref2).split(p0, p1);
+                    p0 = exp2_fast(p0);
+                    p1 = exp2_fast(p1);
+                    sum[(k >> 1) & 3] = sum[(k >> 1) & 3] + Pair(p0, p1);
+                    p[k >> 1] = narrow2<T>(p0, p1);
                 }
+                tmem_st32(s_addr, reinterpret_cast<const float *>(p));
                 {
                     float s0, s1;
                     ((sum[0] + sum[1]) + (sum[2] + sum[3])).split(s0, s1);
@@ -545,25 +568,26 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready + 8 * s);
+            if (elect_one()) mbar_arrive(bar(kProbs + which));
         }
-        if (ok && count > 0) ok = mbar_wait(o_ready + 8 * s, 0, stop);
+        for (int x = 0; x < 2; ++x)
+            if (ok && steps > 0) ok = mbar_wait(bar(kDone + 2 * s + x), (steps / 2 - 1) & 1, stop);
         if (ok && live) {
             tc_after();
             const int part = shared ? split : split * kSlots + s;
             const size_t place = (size_t)(b * a.n_heads + head) * a.parts + part;
-            if (count > 0) {
+            if (steps > 0) {
                 for (int c = 0; c < d; c += 32) {
                     float o[32];
                     __syncwarp();
                     tmem_ld32(o_addr + c, o);
                     tc_wait_ld();
-                    if (row < a.rows)
+                    if (mine)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) store8(a.pv.o + place * d + c + j, o + j);
+                        for (int k = 0; k < 32; k += 8) store8(a.pv.o + place * d + c + k, o + k);
                 }
             }
-            if (row < a.rows) a.pv.ml[place] = make_float2(m, l);
+            if (mine) a.pv.ml[place] = make_float2(m, l);
         }
     }
     tc_before();
@@ -571,7 +595,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     if (threadIdx.x == 0 && s_stop) set_status(a.status, FATHOM_ERR_TIMEOUT);
     if (warp == 2) {
         tc_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "n"(kTmemCols));
     }
 }
 
@@ -596,46 +620,57 @@ EncodeFn encode_fn()
     return fn;
 }
 
-// Boxes of 64 channels by the slots of a page (at most a tile), of one head and page.
-bool encode(CUtensorMap *map, const void *base, const PagedView &kv)
+// A tensor of 16-bit elements, innermost dimension contiguous; strides in
+// elements of the others (of no account where there is one of them).
+template <int RANK>
+bool encode(CUtensorMap *map, const void *base, int dtype, const long long (&size)[RANK],
+            const long long (&stride)[RANK - 1], const int (&box)[RANK])
 {
     EncodeFn fn = encode_fn();
     if (!fn) return false;
-    const int page = 1 << kv.page_shift;
-    const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, (cuuint64_t)page, (cuuint64_t)kv.n_kv_heads,
-                                (cuuint64_t)kv.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)kv.slot_stride * 2, (cuuint64_t)kv.head_stride * 2,
-                                   (cuuint64_t)kv.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(page, kTile), 1, 1}, step[4] = {1, 1, 1, 1};
-    return fn(map,
-              kv.dtype == FATHOM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-              4, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    cuuint64_t dims[RANK], strides[RANK - 1];
+    cuuint32_t boxes[RANK], step[RANK];
+    for (int i = 0; i < RANK; ++i) {
+        dims[i] = (cuuint64_t)size[i];
+        boxes[i] = (cuuint32_t)box[i];
+        step[i] = 1;
+        if (i > 0) strides[i - 1] = (cuuint64_t)(size[i] > 1 ? stride[i - 1] : size[0]) * 2;
+    }
+    return fn(map, dtype == FATHOM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              RANK, const_cast<void *>(base), dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Boxes of 64 channels by the slots of a page (at most a tile), of one head and page.
+bool encode_pages(CUtensorMap *map, const void *base, const PagedView &kv)
+{
+    const int page = 1 << kv.page_shift;
+    return encode<4>(map, base, kv.dtype, {kv.head_dim, page, kv.n_kv_heads, kv.n_pages},
+                     {kv.slot_stride, kv.head_stride, kv.page_stride}, {64, std::min(page, kTile), 1, 1});
+}
 
 template <typename T, int NB>
-cudaError_t launch_shape(const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
+cudaError_t launch_shape(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
                          cudaStream_t stream)
 {
     using Shape = PrefixShape<NB>;
     const cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<T, NB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
     if (e != cudaSuccess) return e;
-    paged_prefix_kernel<T, NB><<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(kmap, vmap, a);
+    paged_prefix_kernel<T, NB><<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(qmap, kmap, vmap, a);
     note_launch();
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_type(const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
+cudaError_t launch_type(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
                         cudaStream_t stream)
 {
     switch ((a.head_dim + 63) / 64) {
-    case 1: return launch_shape<T, 1>(kmap, vmap, a, ctas, stream);
-    case 2: return launch_shape<T, 2>(kmap, vmap, a, ctas, stream);
-    case 3: return launch_shape<T, 3>(kmap, vmap, a, ctas, stream);
-    default: return launch_shape<T, 4>(kmap, vmap, a, ctas, stream);
+    case 1: return launch_shape<T, 1>(qmap, kmap, vmap, a, ctas, stream);
+    case 2: return launch_shape<T, 2>(qmap, kmap, vmap, a, ctas, stream);
+    case 3: return launch_shape<T, 3>(qmap, kmap, vmap, a, ctas, stream);
+    default: return launch_shape<T, 4>(qmap, kmap, vmap, a, ctas, stream);
     }
 }
 
@@ -646,10 +681,10 @@ PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int 
     PrefixPlan p{};
     if (prefix_len == 0) return p;
     const int slots = head_dim <= 128 ? 2 : 1;
-    p.rows = n_seqs * group;
-    p.two_blocks = slots == 2 && p.rows > kRows;
-    const int cta_rows = kRows * (p.two_blocks ? 2 : 1);
-    p.row_groups = (p.rows + cta_rows - 1) / cta_rows;
+    p.slot_seqs = kRows / group;                     // whole sequences: up to 7 rows of 128 are none
+    p.two_blocks = slots == 2 && n_seqs > p.slot_seqs;
+    const int cta_seqs = p.slot_seqs * (p.two_blocks ? 2 : 1);
+    p.row_groups = (n_seqs + cta_seqs - 1) / cta_seqs;
     p.n_tiles = (prefix_len + kTile - 1) / kTile;
     const int units = p.row_groups * n_kv_heads;
     p.splits = std::max(1, std::min(148 / units, p.n_tiles));
@@ -660,8 +695,11 @@ PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int 
 cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const PrefixPlan &p,
                                 const PartsView &pv, int prefix_len, cudaStream_t stream)
 {
-    CUtensorMap kmap, vmap;
-    if (!encode(&kmap, kv.k, kv) || !encode(&vmap, kv.v, kv)) return cudaErrorInvalidValue;
+    CUtensorMap qmap, kmap, vmap;
+    if (!encode_pages(&kmap, kv.k, kv) || !encode_pages(&vmap, kv.v, kv) ||
+        !encode<3>(&qmap, q.q, kv.dtype, {kv.head_dim, kv.n_kv_heads * q.group, q.n_seqs}, {q.q_hs, q.q_ts},
+                   {64, q.group, p.slot_seqs}))
+        return cudaErrorInvalidValue;
     PrefixArgs a{};
     a.q = q;
     a.pv = pv;
@@ -672,7 +710,8 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.page_shift = kv.page_shift;
     a.head_dim = kv.head_dim;
     a.prefix_len = prefix_len;
-    a.rows = p.rows;
+    a.seqs = q.n_seqs;
+    a.slot_seqs = p.slot_seqs;
     a.n_tiles = p.n_tiles;
     a.splits = p.splits;
     a.row_groups = p.row_groups;
@@ -680,8 +719,8 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.parts = p.parts;
     a.status = device_status_ptr();
     const int ctas = p.row_groups * kv.n_kv_heads * p.splits;
-    return kv.dtype == FATHOM_BF16 ? launch_type<__nv_bfloat16>(kmap, vmap, a, ctas, stream)
-                                   : launch_type<__half>(kmap, vmap, a, ctas, stream);
+    return kv.dtype == FATHOM_BF16 ? launch_type<__nv_bfloat16>(qmap, kmap, vmap, a, ctas, stream)
+                                   : launch_type<__half>(qmap, kmap, vmap, a, ctas, stream);
 }
 
 }  // namespace fathom

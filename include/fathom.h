@@ -473,7 +473,7 @@ fathom_status fathom_qk_norm_rope(int32_t n_tokens, int32_t head_dim, const int3
  * element p*page_stride + h*head_stride + s*token_stride + c of k (of v for
  * its value); strides in elements.  k and v: device memory, or pinned host
  * memory used through its device mapping (an offloaded cache; not for
- * fathom_paged_attention); 16-byte aligned, strides multiples of 8.
+ * fathom_paged_attention); 16-byte aligned, strides positive multiples of 8.
  * A page table is device int32 [n_seqs][table_stride]: key j of sequence b
  * lies in slot j % page_size of page page_table[b][j / page_size].
  * Sequences may share pages.  Entries behind a sequence's last key are never
@@ -533,7 +533,7 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  * that sequence gets zeros.  A key on a bad page is skipped (one of the
  * prefix takes part with a K and V of zeros).
  * q, out: rows of n_seqs tokens with G*n_kv_heads heads, in the cache's type,
- * 16-byte aligned, strides multiples of 8; G 1..8.  slopes: device float32
+ * 16-byte aligned, strides positive multiples of 8; G 1..8.  slopes: device float32
  * [G*n_kv_heads].  Scores, softmax and sums are float32; each probability is
  * rounded to the cache's type for its product with V, which is accumulated in
  * float32.  workspace: device memory that no other call in flight uses. */
