@@ -7,11 +7,10 @@
 //   S [128 rows x 128 keys] = Q K^T   both operands K-major in shared memory,
 //   O [128 rows x d]       += P V     P from TMEM, V as it is stored (N-major).
 // A CTA per SM takes one KV head, up to 256 rows and a run of key tiles:
-//   warp 0      copies K and V tiles by TMA, one box per page, through a ring
-//               of stages; a page past the prefix, or a bad one, becomes an
+//   warps 0, 3  copy Q and K, and V, by TMA, one box per page, through a ring of
+//               stages; a page past the prefix, or a bad one, becomes an
 //               out-of-range coordinate, which TMA fills with zeros;
-//   warp 1      issues the products;
-//   warp 2      allocates TMEM;
+//   warps 1, 2  issue the products of a slot each;
 //   warps 4-7   softmax of slot 0, thread = row: S from TMEM, running maximum
 //   warps 8-11  and sum in registers, P back to TMEM over S; slot 1 likewise.
 // Two slots keep the tensor cores busy while a slot's softmax runs.  With more
@@ -281,7 +280,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     // phase's parity does not show.
     constexpr int kFull = 0, kEmpty = kStages, kScores = 2 * kStages, kProbs = kScores + 2 * kSlots,
                   kDone = kProbs + 2 * kSlots, kQueries = kDone + 2 * kSlots, kDrained = kQueries + 1,
-                  kBarriers = kDrained + 1;
+                  kBarriers = kDrained + kSlots;
     __shared__ alignas(8) uint64_t s_bar[kBarriers];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
@@ -303,7 +302,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     const uint32_t o_col = kSlots * kTile;                      // O of slot s at o_col + s*d
 
     if (warp == 0) {
-        for (int i = lane; i < kBarriers; i += 32) mbar_init(bar(i), i >= kProbs && i < kDone ? 4 : 1);
+        // a stage that both slots read is freed by both; P comes from four warps
+        for (int i = lane; i < kBarriers; i += 32)
+            mbar_init(bar(i), i >= kEmpty && i < kScores ? (shared ? kSlots : 1) : i >= kProbs && i < kDone ? 4 : 1);
         if (lane == 0) s_stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -319,8 +320,13 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             return lane < boxes && key < a.prefix_len ? a.table[key >> shift] : a.n_pages;
         };
         int page = page_of(0);
+        __syncwarp();
+        if (elect_one()) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+            if (keys) asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
+        }
+        __syncwarp();
         if (keys) {
-            __syncwarp();
             // the others wait for this, and for TMEM; the first copies of Q and K do not
             asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory");
             const int slots = shared ? kSlots : 1, box_bytes = a.slot_seqs * G * 128;
@@ -386,9 +392,10 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             __syncwarp();
         }
     } else if (warp < 4) {
-        // by a warp that does nothing else: after code for one of its lanes a warp need not be
-        // together again for an aligned instruction
-        if (warp == 2) {
+        // ---------------------------------------------------- products: a warp for each slot, so
+        // that one waits and prepares while the other's are in the pipe
+        const int me = warp - 1;
+        if (warp == 1) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                              smem_u32(&s_tmem)),
                          "n"(kTmemCols)
@@ -397,86 +404,75 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             tc_before();
         }
         asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
-        if (warp == 1) {
-            // ------------------------------------------------ products
+        if (me < kSlots) {
             tc_after();
-            const uint32_t tmem = s_tmem;
             const uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
             const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | ((128u >> 4) << 24);
             const uint32_t idesc_qk = common | ((uint32_t)(kStep >> 3) << 17);
             const uint32_t idesc_pv = common | (1u << 16) | ((uint32_t)(d >> 3) << 17);
-            const uint64_t k_ring = umma_desc(ring, 16), v_ring = umma_desc(ring, kBlockBytes);
-            const uint64_t q_first = umma_desc(q_addr, 16);
             constexpr int kStageStep = kTileBytes >> 4, kHalfStep = (kStep * 128) >> 4;
+            const uint64_t k_ring = umma_desc(ring, 16), v_ring = umma_desc(ring, kBlockBytes);
+            const uint64_t q_desc = umma_desc(q_addr, 16) + (shared ? me * kStageStep : 0);
+            const uint32_t s_col = s_tmem + me * kTile, o_at = s_tmem + o_col + me * d;
+            const int takers = walk.takers(), steps = walk.steps(me);
             Place<kStages> at;
-            int k_stage[kSlots] = {}, v_stage[kSlots] = {};
-            int steps[kSlots];
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) steps[s] = walk.steps(s);
+            int k = 0, v = 0;                                   // stages of the tiles in use
             bool ok = mbar_wait(bar(kQueries), 0, stop);
-            const auto take = [&](int &stage) {
-                stage = at.stage;
-                ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop);
+            const auto take = [&](bool mine, int &stage) {
+                if (mine) {
+                    stage = at.stage;
+                    ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop);
+                }
                 at.next();
             };
             // S = Q K^T of step j, by one lane
-            const auto scores = [&](int j, int s, int stage) {
-                const uint64_t k_desc = k_ring + stage * kStageStep + (j & 1) * kHalfStep;
-                const uint64_t q_desc = q_first + (shared ? s * kStageStep : 0);
+            const auto scores = [&](int j) {
+                const uint64_t k_desc = k_ring + k * kStageStep + (j & 1) * kHalfStep;
 #pragma unroll
-                for (int k = 0; k < NB * 4; ++k) {              // 16 channels: 32 bytes of a 64-channel block
-                    const int off = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
-                    if (k < d / 16)
-                        umma_ss(tmem + s * kTile + (j & 1) * kStep, q_desc + off, k_desc + off, idesc_qk, k > 0);
+                for (int x = 0; x < NB * 4; ++x) {              // 16 channels: 32 bytes of a 64-channel block
+                    const int off = ((x >> 2) * kBlockBytes + (x & 3) * 32) >> 4;
+                    if (x < d / 16) umma_ss(s_col + (j & 1) * kStep, q_desc + off, k_desc + off, idesc_qk, x > 0);
                 }
-                umma_commit(bar(kScores + 2 * s + (j & 1)));
+                umma_commit(bar(kScores + 2 * me + (j & 1)));
             };
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                if (steps[s] == 0) continue;
-                if (!shared || s == 0) take(k_stage[s]);
-                const int k = shared ? k_stage[0] : k_stage[s];
+            for (int s = 0; s < takers; ++s)
+                if (walk.steps(s) > 0) take(shared || s == me, k);
+            tc_after();
+            if (ok && steps > 0 && elect_one()) {
+                scores(0);
+                scores(1);
+                umma_commit(bar(kEmpty + k));
+            }
+            __syncwarp();
+            for (int j = 0; j < steps && ok; ++j) {
+                const bool more = j + 2 < steps;
+                if (!(j & 1))
+                    for (int s = 0; s < takers; ++s) {
+                        if (j < walk.steps(s)) take(shared || s == me, v);
+                        if (j + 2 < walk.steps(s)) take(shared || s == me, k);
+                    }
+                const uint64_t v_desc = v_ring + v * kStageStep + (j & 1) * kHalfStep;
+                ok = ok && mbar_wait(bar(kProbs + 2 * me + (j & 1)), (j >> 1) & 1, stop);
                 tc_after();
                 if (ok && elect_one()) {
-                    scores(0, s, k);
-                    scores(1, s, k);
-                    if (!shared || s == kSlots - 1) umma_commit(bar(kEmpty + k));
+                    // O += P V of step j; then S of step j + 2 goes where P was
+#pragma unroll
+                    for (int x = 0; x < kStep / 16; ++x)        // 16 keys: 2048 bytes of V, 8 columns of P
+                        umma_ts(o_at, s_col + (j & 1) * kStep + x * 8, v_desc + x * (2048 >> 4), idesc_pv,
+                                j > 0 || x > 0);
+                    umma_commit(bar(kDone + 2 * me + (j & 1)));
+                    if (j & 1) umma_commit(bar(kEmpty + v));
+                    if (more) {
+                        scores(j + 2);
+                        if (j & 1) umma_commit(bar(kEmpty + k));
+                    }
                 }
                 __syncwarp();
             }
-            for (int j = 0; j < steps[0] && ok; ++j)
-#pragma unroll
-                for (int s = 0; s < kSlots; ++s) {
-                    if (j >= steps[s]) continue;
-                    const bool more = j + 2 < steps[s];
-                    if (!(j & 1) && (!shared || s == 0)) {
-                        take(v_stage[s]);
-                        if (more) take(k_stage[s]);
-                    }
-                    ok = ok && mbar_wait(bar(kProbs + 2 * s + (j & 1)), (j >> 1) & 1, stop);
-                    tc_after();
-                    const int v = shared ? v_stage[0] : v_stage[s], k = shared ? k_stage[0] : k_stage[s];
-                    const bool free = (j & 1) && (!shared || s == kSlots - 1);
-                    const uint64_t v_desc = v_ring + v * kStageStep + (j & 1) * kHalfStep;
-                    if (ok && elect_one()) {
-                        // O += P V of step j; then S of step j + 2 goes where P was
-#pragma unroll
-                        for (int x = 0; x < kStep / 16; ++x)    // 16 keys: 2048 bytes of V, 8 columns of P
-                            umma_ts(tmem + o_col + s * d, tmem + s * kTile + (j & 1) * kStep + x * 8,
-                                    v_desc + x * (2048 >> 4), idesc_pv, j > 0 || x > 0);
-                        umma_commit(bar(kDone + 2 * s + (j & 1)));
-                        if (free) umma_commit(bar(kEmpty + v));
-                        if (more) {
-                            scores(j + 2, s, k);
-                            if (free) umma_commit(bar(kEmpty + k));
-                        }
-                    }
-                    __syncwarp();
-                }
             if (!ok) {                                          // let the products end
-                if (elect_one()) umma_commit(bar(kDrained));
+                if (elect_one()) umma_commit(bar(kDrained + me));
                 __syncwarp();
-                wait_anyway(bar(kDrained), 0);
+                wait_anyway(bar(kDrained + me), 0);
             }
         }
     } else {
@@ -593,7 +589,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     tc_before();
     __syncthreads();
     if (threadIdx.x == 0 && s_stop) set_status(a.status, FATHOM_ERR_TIMEOUT);
-    if (warp == 2) {
+    if (warp == 1) {
+        __syncwarp();
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "n"(kTmemCols));
     }
