@@ -42,6 +42,7 @@ constexpr int kBlockBytes = kTile * 128;         // 128 rows of 64 channels (128
 constexpr unsigned long long kWaitNs = 500000000ull;
 constexpr unsigned long long kSettleNs = 1000000ull;   // for copies under way after a stop
 constexpr int kTmemCols = 512;
+constexpr int kStageBytes = 4 * 32 * 128;        // 32 channels of a slot's rows in float32
 
 template <int NB>
 struct PrefixShape {                             // NB = 64-channel blocks of a row
@@ -49,7 +50,10 @@ struct PrefixShape {                             // NB = 64-channel blocks of a 
     static constexpr int kStages = NB == 1 ? 8 : NB == 2 ? 5 : NB == 3 ? 3 : 2;
     static constexpr int kTileBytes = NB * kBlockBytes;
     static constexpr int kThreads = 128 + 128 * kSlots;
-    static constexpr int kSmem = (kSlots + kStages) * kTileBytes + 1024;
+    // Q of the slots; where they have the same rows, one tile and the stages of both
+    static constexpr int kQueryBytes = kSlots == 2 ? (kTileBytes > 2 * kStageBytes ? kTileBytes : 2 * kStageBytes) + kTileBytes
+                                                   : kTileBytes;
+    static constexpr int kSmem = kQueryBytes + kStages * kTileBytes + 1024;
 };
 
 struct PrefixArgs {
@@ -58,7 +62,7 @@ struct PrefixArgs {
     ScoreArgs score;
     const int32_t *table;                        // the first row of the page table
     int n_heads, n_pages, page_shift, head_dim;
-    int prefix_len, seqs, slot_seqs, n_tiles, splits, row_groups, two_blocks, parts;
+    int prefix_len, seqs, slot_seqs, split_tiles, split_rest, two_blocks, parts;
     int *status;
 };
 
@@ -230,14 +234,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
         : "memory");
 }
 
-// Whole 32-byte sectors: each lane writes another row.
-__device__ __forceinline__ void store8(float *p, const float *x)
-{
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]),
-                 "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
-
 // Which tiles the slots of a CTA take, each in two steps of kStep keys.  The
 // warps that copy and the one that issues products walk the same order: K of
 // every slot's first tile, then at each even step j, slot by slot, V of the
@@ -264,7 +260,7 @@ struct Place {
     }
 };
 
-// grid: (row group, KV head) fastest, then the run of tiles
+// grid (row groups, KV heads, runs of tiles)
 template <typename T, int NB>
 __global__ void __launch_bounds__(PrefixShape<NB>::kThreads, 1)
 paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -285,14 +281,12 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
-    const uint32_t q_addr = base, ring = base + kSlots * kTileBytes, bars = smem_u32(s_bar);
+    const uint32_t q_addr = base, ring = base + Shape::kQueryBytes, bars = smem_u32(s_bar);
     const auto bar = [&](int i) { return bars + 8 * i; };
 
-    const int per = gridDim.x / a.splits;                       // row groups * KV heads
-    const int split = blockIdx.x / per, unit = blockIdx.x - split * per;
-    const int h = unit / a.row_groups, group = unit - h * a.row_groups;
-    const int t0 = (int)((long long)split * a.n_tiles / a.splits);
-    const int t1 = (int)((long long)(split + 1) * a.n_tiles / a.splits);
+    const int group = blockIdx.x, h = blockIdx.y, split = blockIdx.z;
+    const int t0 = split * a.split_tiles + min(split, a.split_rest);
+    const int t1 = t0 + a.split_tiles + (split < a.split_rest ? 1 : 0);
     const bool shared = a.two_blocks || kSlots == 1;
     const Walk walk{t1 - t0, kSlots, shared};
     const int seq0 = group * a.slot_seqs * (shared ? kSlots : 1);   // of slot 0
@@ -355,20 +349,17 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     p = a.n_pages;
                 }
                 page = page_of(tile + 1);
-                int pages[16];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) pages[x] = __shfl_sync(0xFFFFFFFFu, p, x);
                 const uint32_t dst = ring + at.stage * kTileBytes, full = bar(kFull + at.stage);
                 const int slot0 = ((t0 + tile) * kTile) & ((1 << shift) - 1);   // a page may hold several tiles
-                if (elect_one()) {
-                    mbar_expect(full, kTileBytes);
+                if (elect_one()) mbar_expect(full, kTileBytes);
+                __syncwarp();
+#pragma unroll 1
+                for (int x = 0; x < boxes; ++x) {
+                    const int px = __shfl_sync(0xFFFFFFFFu, p, x);
+                    if (elect_one())
 #pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        if (x < boxes)
-#pragma unroll
-                            for (int cb = 0; cb < NB; ++cb)
-                                tma_load(dst + cb * kBlockBytes + x * box * 128, map, full, cb * 64, slot0, h,
-                                         pages[x]);
+                        for (int cb = 0; cb < NB; ++cb)
+                            tma_load(dst + cb * kBlockBytes + x * box * 128, map, full, cb * 64, slot0, h, px);
                 }
                 __syncwarp();
                 ++issued;
@@ -571,19 +562,41 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         if (ok && live) {
             tc_after();
             const int part = shared ? split : split * kSlots + s;
-            const size_t place = (size_t)(b * a.n_heads + head) * a.parts + part;
+            const long long place = mine ? (long long)(b * a.n_heads + head) * a.parts + part : -1;
+            if (mine) a.pv.ml[place] = make_float2(m, l);
             if (steps > 0) {
+                // 32 channels of the warp's 32 rows at a time through shared memory, so that a store
+                // is four rows of 128 bytes (a lane's own row at a time: 32 rows, 1.6 us longer)
+                // the slot's own tile of Q, done with, or room behind the one that the other may read
+                const uint32_t stage = q_addr + (shared ? s * kTileBytes : kTileBytes + s * kStageBytes) +
+                                       (warp & 3) * (kStageBytes / 4);
+                long long to[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) to[x] = __shfl_sync(0xFFFFFFFFu, place, 4 * x + (lane >> 3));
+#pragma unroll 1
                 for (int c = 0; c < d; c += 32) {
                     float o[32];
                     __syncwarp();
                     tmem_ld32(o_addr + c, o);
                     tc_wait_ld();
-                    if (mine)
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) store8(a.pv.o + place * d + c + k, o + k);
+                    for (int k = 0; k < 8; ++k)
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         stage + lane * 128 + ((k ^ (lane & 7)) << 4)),
+                                     "f"(o[4 * k]), "f"(o[4 * k + 1]), "f"(o[4 * k + 2]), "f"(o[4 * k + 3])
+                                     : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int row = 4 * x + (lane >> 3), k = lane & 7;
+                        float4 v;
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                                     : "r"(stage + row * 128 + ((k ^ (row & 7)) << 4)));
+                        if (to[x] >= 0) *reinterpret_cast<float4 *>(a.pv.o + to[x] * d + c + 4 * k) = v;
+                    }
                 }
             }
-            if (mine) a.pv.ml[place] = make_float2(m, l);
         }
     }
     tc_before();
@@ -647,7 +660,7 @@ bool encode_pages(CUtensorMap *map, const void *base, const PagedView &kv)
 }
 
 template <typename T, int NB>
-cudaError_t launch_shape(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
+cudaError_t launch_shape(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, dim3 ctas,
                          cudaStream_t stream)
 {
     using Shape = PrefixShape<NB>;
@@ -660,7 +673,7 @@ cudaError_t launch_shape(const CUtensorMap &qmap, const CUtensorMap &kmap, const
 }
 
 template <typename T>
-cudaError_t launch_type(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, int ctas,
+cudaError_t launch_type(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const PrefixArgs &a, dim3 ctas,
                         cudaStream_t stream)
 {
     switch ((a.head_dim + 63) / 64) {
@@ -683,9 +696,10 @@ PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int 
     const int cta_seqs = p.slot_seqs * (p.two_blocks ? 2 : 1);
     p.row_groups = (n_seqs + cta_seqs - 1) / cta_seqs;
     p.n_tiles = (prefix_len + kTile - 1) / kTile;
-    const int units = p.row_groups * n_kv_heads;
-    p.splits = std::max(1, std::min(148 / units, p.n_tiles));
-    p.parts = p.splits * (slots == 2 && !p.two_blocks ? 2 : 1);
+    // one wave of CTAs, of a tile for every slot at least
+    const int units = p.row_groups * n_kv_heads, both = slots == 2 && !p.two_blocks ? 2 : 1;
+    p.splits = std::max(1, std::min(148 / units, p.n_tiles / both));
+    p.parts = p.splits * both;
     return p;
 }
 
@@ -709,13 +723,12 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.prefix_len = prefix_len;
     a.seqs = q.n_seqs;
     a.slot_seqs = p.slot_seqs;
-    a.n_tiles = p.n_tiles;
-    a.splits = p.splits;
-    a.row_groups = p.row_groups;
+    a.split_tiles = p.n_tiles / p.splits;
+    a.split_rest = p.n_tiles % p.splits;
     a.two_blocks = p.two_blocks;
     a.parts = p.parts;
     a.status = device_status_ptr();
-    const int ctas = p.row_groups * kv.n_kv_heads * p.splits;
+    const dim3 ctas(p.row_groups, kv.n_kv_heads, p.splits);
     return kv.dtype == FATHOM_BF16 ? launch_type<__nv_bfloat16>(qmap, kmap, vmap, a, ctas, stream)
                                    : launch_type<__half>(qmap, kmap, vmap, a, ctas, stream);
 }
