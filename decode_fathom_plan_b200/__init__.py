@@ -347,14 +347,15 @@ def _dtype_code(dtype) -> int:
 def fathom_rotary_turns(rotary_dim: int, base: float = 10000.0, scaling: int = FATHOM_ROTARY_PLAIN,
                         factor: float = 1.0, original_len: int = 1, beta_fast: float = 32.0,
                         beta_slow: float = 1.0):
-    """-> (list of rotary_dim/2 turns per position, magnitude)."""
-    turns = (ctypes.c_double * max(1, int(rotary_dim) // 2))()
+    """-> (turns per position, a host float64 tensor [rotary_dim/2]; magnitude)."""
+    import torch
+    turns = torch.empty(max(1, int(rotary_dim) // 2), dtype=torch.float64)
     magnitude = ctypes.c_float()
-    _check(load_library().fathom_rotary_turns(turns, ctypes.byref(magnitude), int(rotary_dim),
-                                              float(base), int(scaling), float(factor),
-                                              int(original_len), float(beta_fast),
+    _check(load_library().fathom_rotary_turns(turns.data_ptr(), ctypes.byref(magnitude),
+                                              int(rotary_dim), float(base), int(scaling),
+                                              float(factor), int(original_len), float(beta_fast),
                                               float(beta_slow)), "fathom_rotary_turns")
-    return list(turns), magnitude.value
+    return turns, magnitude.value
 
 
 def fathom_qk_norm_rope(q, k, pos, q_out, k_out, rotary=None, q_weight=None, k_weight=None,
@@ -587,7 +588,7 @@ class RotaryTable:
                                                original_len, beta_fast, beta_slow)
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else device)
-        self.turns = torch.tensor(turns, dtype=torch.float64, device=self.device)
+        self.turns = turns.to(self.device)
         self.magnitude = magnitude
         self.device_index = self.device.index
         self.desc = fathom_rotary(self.turns.data_ptr(), rotary_dim, int(interleaved), magnitude)

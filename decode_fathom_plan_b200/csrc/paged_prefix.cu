@@ -689,7 +689,14 @@ cudaError_t launch_type(const CUtensorMap &qmap, const CUtensorMap &kmap, const 
 PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int prefix_len)
 {
     PrefixPlan p{};
-    if (prefix_len == 0) return p;
+    // Below some 8 MB of repeated reads, which mostly hit L2, each sequence reads the prefix for
+    // itself: this kernel takes 10 us for the least prefix, the sequences' own 7 us.  Measured with
+    // it and without at 8 KV heads of 128: 2 sequences of 1024 keys (4 MB) 9.9 and 8.3 us, of 4096
+    // (17 MB) 12.3 and 14.1; 8 of 256 (7 MB) 10.3 and 9.9, of 1024 (29 MB) 10.7 and 14.4, of 16384
+    // 28 and 66; at 2 heads of 64 8 of 1024 (4 MB) 9.6 and 7.4, 2 of 16384 (8 MB) 10.7 and 11.3; at
+    // 4 of 256 2 of 1024 (4 MB) 10.4 and 9.2, of 4096 (17 MB) 13.7 and 14.5.
+    const long long repeated = (long long)(n_seqs - 1) * prefix_len * n_kv_heads * head_dim * 4;
+    if (repeated < (8ll << 20)) return p;
     const int slots = head_dim <= 128 ? 2 : 1;
     p.slot_seqs = kRows / group;                     // whole sequences: up to 7 rows of 128 are none
     p.two_blocks = slots == 2 && n_seqs > p.slot_seqs;

@@ -47,7 +47,7 @@ def test_rotation_tables(lib, kind, factor, rd):
     code = fp.RotaryTable._SCALINGS[kind]
     got, mag = fp.fathom_rotary_turns(rd, 1e6, code, factor, 32768, 32.0, 1.0)
     freq, want_mag = po.turns(rd, 1e6, kind, factor, 32768, 32.0, 1.0)
-    assert np.allclose(np.array(got) * 2 * math.pi, freq, rtol=1e-12, atol=0)
+    assert np.allclose(got.numpy() * 2 * math.pi, freq, rtol=1e-12, atol=0)
     assert abs(mag - want_mag) <= 2.0 ** -24 * want_mag
 
 

@@ -312,6 +312,160 @@ def test_attention(lens, prefix, H, G, d, page, dtype, tm, cap, slopes):
         assert status() == fp.FATHOM_OK
 
 
+def few_rows(b, n=12):
+    """Some rows of a batch, the first, the last and the borders of 128-row blocks among them."""
+    hq = b.H * b.G
+    every = [(s, i) for s in range(len(b.lens)) for i in range(hq)]
+    per = 128 // b.G                                    # sequences of a block
+    border = [(s, i) for k in (1, 2, 3) for s in (k * per - 1, k * per) if s < len(b.lens) for i in (0, hq - 1)]
+    rng = np.random.default_rng(n)
+    return set(border + [every[0], every[-1]] + [every[j] for j in rng.choice(len(every), min(n, len(every)), replace=False)])
+
+
+def check_rows(b, rows, cap=0.0, slopes=None):
+    want, tol = b.expect(cap, slopes, rows=rows)
+    at = tuple(np.array(sorted(rows)).T)
+    check(b.out.cpu()[at], want[at], tol[at])
+
+
+# prefixes whose repeated reads, 4 bytes * d * H * prefix * (sequences - 1), pass 8 MB: multiplied
+# with the queries of all sequences at once
+SHARED = [
+    # lens, prefix, H, G, d, page, dtype, token_major, cap, slopes
+    ([2100, 2049], 2048, 8, 1, 128, 16, BF16, False, 0.0, False),
+    ([1000 + i for i in range(33)], 992, 2, 4, 128, 32, BF16, False, 0.0, False),
+    ([512 + 3 * i for i in range(40)], 512, 1, 7, 128, 16, F16, True, 0.0, True),
+    ([512] * 70, 512, 1, 8, 64, 64, F16, False, 0.0, False),
+    ([1160 + i for i in range(20)], 1160, 2, 5, 96, 8, BF16, False, 50.0, True),
+    ([4112 + 7 * i for i in range(9)], 4112, 2, 8, 32, 16, F16, False, 0.0, False),
+    ([2050, 2049, 0, 2048, 2500], 2048, 2, 6, 256, 16, BF16, False, 0.0, False),
+    ([640 + i for i in range(35)], 640, 1, 4, 160, 128, F16, False, 0.0, True),
+    ([1152 + i for i in range(17)], 1152, 1, 8, 192, 16, BF16, True, 20.0, False),
+    ([1024 + 500 * (i % 2) for i in range(12)], 1024, 1, 3, 224, 1024, F16, False, 0.0, False),
+    ([136 + i % 5 for i in range(130)], 136, 1, 1, 128, 8, BF16, False, 0.0, True),
+    ([8200, 0, 8192], 8192, 8, 2, 64, 16, BF16, True, 0.0, False),
+    ([4096 + 11 * i for i in range(40)], 4096, 8, 4, 128, 256, BF16, False, 0.0, False),
+    ([33000, 32768], 32768, 1, 8, 128, 16, F16, False, 30.0, True),
+    ([16384 + i for i in range(3)], 16384, 4, 2, 256, 32, F16, False, 0.0, False),
+]
+
+
+@pytest.mark.parametrize("lens,prefix,H,G,d,page,dtype,tm,cap,slopes", SHARED)
+def test_shared_prefix(lens, prefix, H, G, d, page, dtype, tm, cap, slopes):
+    assert 4 * d * H * prefix * (len(lens) - 1) >= 8 << 20
+    b = Batch(lens, prefix, H, G, d, page, dtype, tm, 31 + d + len(lens))
+    sl = b.slopes().cuda() if slopes else None
+    b.attention(cap=cap, slopes=sl)
+    rows = few_rows(b)
+    check_rows(b, rows, cap, sl)
+    assert status() == fp.FATHOM_OK
+    for s, n in enumerate(lens):
+        assert n or (b.out[s] == 0).all()
+    first = b.out.clone()
+    for _ in range(4):
+        b.out.fill_(math.nan)
+        b.attention(cap=cap, slopes=sl)
+        assert torch.equal(b.out, first)
+    # the same batch with nothing said of the prefix: each sequence reads it for itself
+    b.prefix = 0
+    b.attention(cap=cap, slopes=sl)
+    check_rows(b, rows, cap, sl)
+    if max(lens) + 3000 < 40000:
+        b.prefix = prefix
+        b.table_t = torch.nn.functional.pad(b.table_t, (0, -(-3000 // page)), value=-9)
+        b.attention(max_len=max(lens) + 3000, cap=cap, slopes=sl)
+        check_rows(b, rows, cap, sl)
+        assert status() == fp.FATHOM_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("G,d", [(1, 128), (4, 64), (2, 256)])
+def test_shared_prefix_of_growing_scores(dtype, G, d):
+    """Every step of every slot renews its maximum and rescales its sums."""
+    n, prefix, H = 16500, 16384, 8 if d < 256 else 4
+    b = Batch([n, n - 7], prefix, H, G, d, 16, dtype, False, 3)
+    ramp = torch.linspace(0.5, 24.0, n).to(dtype).cuda()
+    for s, m in enumerate(b.lens):
+        j = np.arange(m)
+        pg, at = torch.from_numpy(b.table[s, j // 16]).long().cuda(), torch.from_numpy(j % 16).cuda()
+        b.kv.k[pg, :, at] = ramp[:m, None, None].expand(m, H, d).contiguous()
+    b.q.fill_(1.0)
+    b.k64 = po.f64(b.kv.k)
+    b.attention()
+    check_rows(b, few_rows(b, 4))
+    # and a scale below zero, under which they fall
+    b.scale = -b.scale
+    b.attention()
+    for s, i in sorted(few_rows(b, 2)):
+        ks, vs = (po.gather(p, b.table[s], np.arange(b.lens[s]), i // G, 16) for p in (b.k64, b.v64))
+        q = po.f64(b.q)[s, i]
+        want, err = po.attend(-q, ks, vs, np.zeros(b.lens[s]), -b.scale, p_step=po.HALF_STEP[dtype],
+                              p_tiny=po.TINY[dtype] * 2.0 ** 8)
+        check(b.out[s, i], want, err + po.HALF_STEP[dtype] * np.abs(want) * 1.01 + po.TINY[dtype])
+
+
+def test_shared_prefix_refusals_on_the_device():
+    b = Batch([2100, 2060, 2090], 2048, 8, 2, 64, 16, F16, False, 9)
+    good = b.table_t.clone()
+    b.attention()
+    rows = few_rows(b)
+    check_rows(b, rows)
+    clean = b.out.clone()
+    b.lens_t[1] = 2047                              # inside the prefix
+    b.attention()
+    assert status() == fp.FATHOM_ERR_INVALID_ARG
+    assert (b.out[1] == 0).all() and torch.equal(b.out[[0, 2]], clean[[0, 2]])
+    b.lens_t[1] = 2060
+    for page in (-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1, b.kv.k.shape[0]):
+        b.table_t[:, 77] = page
+        b.attention()
+        assert status() == fp.FATHOM_ERR_INVALID_ARG
+        assert torch.isfinite(b.out).all()
+        b.table_t.copy_(good)
+    b.kv.v[b.table[0, 5], 3, 2, 7] = math.inf        # one value of a prefix key: its channel of its head
+    b.attention()
+    inf = ~torch.isfinite(b.out)
+    assert inf[:, 6:8, 7].all() and not inf[:, :6].any() and not inf[:, 8:].any()
+    assert not inf[:, 6:8, :7].any() and not inf[:, 6:8, 8:].any()
+    assert status() == fp.FATHOM_OK
+
+
+def test_shared_prefix_captured_and_on_two_streams():
+    bs = [Batch([2300 + i, 2200, 2048, 0], 2048, 8, 2, 64, 16, BF16, False, 40 + i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    for b in bs:
+        b.table_t = torch.nn.functional.pad(b.table_t, (0, 10), value=-9)
+        b.space = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+        b.attention(max_len=2400, ws=b.space)
+    torch.cuda.synchronize()
+    graphs = []
+    for b, s in zip(bs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            g.capture_begin()
+            b.attention(max_len=2400, ws=b.space)
+            g.capture_end()
+        graphs.append(g)
+    for r in range(3):
+        for b in bs:
+            b.lens = [2049 + 30 * r, 0, 2300, 2048]
+            b.lens_t.copy_(torch.tensor(b.lens, dtype=torch.int32))
+            b.table_t[:, 128:] = b.table_t[:1, 128:]            # all read the first one's own pages
+            b.q.copy_(randn(list(b.q.shape), BF16, 90 + r))
+            b.out.fill_(math.nan)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for b in bs:
+            b.table = b.table_t.cpu().numpy()
+            b.lens = [2049 + 30 * r, 0, 2300, 2048]
+            check_rows(b, few_rows(b))
+        assert status() == fp.FATHOM_OK
+
+
 @pytest.mark.parametrize("prefix", [0, 512])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_attention_of_sharp_and_growing_scores(prefix, dtype):
