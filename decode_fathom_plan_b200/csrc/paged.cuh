@@ -125,8 +125,11 @@ __device__ __forceinline__ void store_row(const PagedQuery &q, int b, int head, 
 
 // ------------------------------------------------- kernels that follow closely
 // A kernel launched by launch_overlapped may start once every CTA of the one
-// before it has called let_next_kernel_start() or ended; what it reads of that
-// kernel, or of those before it, it reads after wait_for_earlier_kernels().
+// before it in the stream has called let_next_kernel_start() or ended; what it
+// reads or overwrites of that kernel, or of those before it, it touches after
+// wait_for_earlier_kernels(), which waits for them to end.  (So a kernel that
+// lets the next one start does it after its own wait.)  All that is gained is
+// the launch: a microsecond or two from one small kernel to the next.
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

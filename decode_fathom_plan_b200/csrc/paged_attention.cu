@@ -137,6 +137,8 @@ paged_split_kernel(const SplitArgs a)
     __shared__ float s_m[kSplitWarps][8], s_l[kSplitWarps][8];
     __shared__ alignas(16) float s_o[kSplitWarps][8][d];
     __shared__ uint4 s_q[kSharedQ ? E : 1][32];
+    // beside the kernel of the prefix nothing is read that an earlier one of this call writes
+    if (!a.others) wait_for_earlier_kernels();
     let_next_kernel_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -412,9 +414,7 @@ paged_split_kernel(const SplitArgs a)
 template <typename T, int E>
 cudaError_t launch_one(const SplitArgs &a, int ctas, cudaStream_t stream)
 {
-    if (a.others) return launch_overlapped(paged_split_kernel<T, E>, dim3(ctas), kSplitThreads, 0, stream, a);
-    paged_split_kernel<T, E><<<ctas, kSplitThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(paged_split_kernel<T, E>, dim3(ctas), kSplitThreads, 0, stream, a);
 }
 
 template <typename T>

@@ -269,6 +269,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     using Shape = PrefixShape<NB>;
     constexpr int kSlots = Shape::kSlots, kStages = Shape::kStages, kTileBytes = Shape::kTileBytes;
     constexpr int kThreads = Shape::kThreads;
+    wait_for_earlier_kernels();
     let_next_kernel_start();
     extern __shared__ unsigned char s_raw[];
     // Of slot s and step j: S, P and the product with V each at 2*s + (j & 1) of their barriers,
@@ -667,9 +668,9 @@ cudaError_t launch_shape(const CUtensorMap &qmap, const CUtensorMap &kmap, const
     const cudaError_t e = cudaFuncSetAttribute(paged_prefix_kernel<T, NB>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
     if (e != cudaSuccess) return e;
-    paged_prefix_kernel<T, NB><<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(qmap, kmap, vmap, a);
     note_launch();
-    return cudaGetLastError();
+    return launch_overlapped(paged_prefix_kernel<T, NB>, ctas, Shape::kThreads, Shape::kSmem, stream, qmap, kmap, vmap,
+                             a);
 }
 
 template <typename T>

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kSparseThreads)
 paged_sparse_kernel(const SparseArgs a)
 {
     constexpr int d = 32 * E;
+    wait_for_earlier_kernels();
     let_next_kernel_start();
     __shared__ float s_m[kSparseWarps], s_l[kSparseWarps];
     __shared__ alignas(16) float s_o[kSparseWarps][d];
@@ -204,17 +205,18 @@ paged_sparse_kernel(const SparseArgs a)
 }
 
 template <typename T>
-void launch_sparse(const SparseArgs &a, dim3 grid, cudaStream_t stream)
+cudaError_t launch_sparse(const SparseArgs &a, dim3 grid, cudaStream_t stream)
 {
+    const auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, kSparseThreads, 0, stream, a); };
     switch (a.kv.head_dim / 32) {
-    case 1: paged_sparse_kernel<T, 1><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    case 2: paged_sparse_kernel<T, 2><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    case 3: paged_sparse_kernel<T, 3><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    case 4: paged_sparse_kernel<T, 4><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    case 5: paged_sparse_kernel<T, 5><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    case 6: paged_sparse_kernel<T, 6><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    case 7: paged_sparse_kernel<T, 7><<<grid, kSparseThreads, 0, stream>>>(a); break;
-    default: paged_sparse_kernel<T, 8><<<grid, kSparseThreads, 0, stream>>>(a); break;
+    case 1: return go(paged_sparse_kernel<T, 1>);
+    case 2: return go(paged_sparse_kernel<T, 2>);
+    case 3: return go(paged_sparse_kernel<T, 3>);
+    case 4: return go(paged_sparse_kernel<T, 4>);
+    case 5: return go(paged_sparse_kernel<T, 5>);
+    case 6: return go(paged_sparse_kernel<T, 6>);
+    case 7: return go(paged_sparse_kernel<T, 7>);
+    default: return go(paged_sparse_kernel<T, 8>);
     }
 }
 
@@ -251,12 +253,9 @@ cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const 
     if (!a.direct) a.pv = parts_carve(ws, (size_t)rows * runs, kv.head_dim);
     a.status = device_status_ptr();
     const dim3 grid(runs, n_heads, q.n_seqs);
-    if (kv.dtype == FATHOM_BF16)
-        launch_sparse<__nv_bfloat16>(a, grid, stream);
-    else
-        launch_sparse<__half>(a, grid, stream);
     note_launch();
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = kv.dtype == FATHOM_BF16 ? launch_sparse<__nv_bfloat16>(a, grid, stream)
+                                                  : launch_sparse<__half>(a, grid, stream);
     if (e != cudaSuccess || a.direct) return e;
     MergeArgs m{};
     m.pv = a.pv;

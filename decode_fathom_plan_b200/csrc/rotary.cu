@@ -206,6 +206,8 @@ rows_kernel(const RowsArgs a)
     const int lane = threadIdx.x & (a.lanes - 1), grp = threadIdx.x / a.lanes;
     const int groups = kRowThreads / a.lanes;
     const int step_t = groups / heads, step_h = groups - step_t * heads;
+    wait_for_earlier_kernels();
+    let_next_kernel_start();
 
     // offsets of the lane's units in a row
     int at[P::kIter], at2[P::kIter];
@@ -362,14 +364,13 @@ rows_kernel(const RowsArgs a)
 }
 
 template <int VEC>
-void launch_rows_vec(const RowsArgs &a, int dtype, int blocks, cudaStream_t stream)
+cudaError_t launch_rows_vec(const RowsArgs &a, int dtype, int blocks, cudaStream_t stream)
 {
     if (dtype == FATHOM_F32)
-        rows_kernel<VEC, float><<<blocks, kRowThreads, 0, stream>>>(a);
-    else if (dtype == FATHOM_BF16)
-        rows_kernel<VEC, __nv_bfloat16><<<blocks, kRowThreads, 0, stream>>>(a);
-    else
-        rows_kernel<VEC, __half><<<blocks, kRowThreads, 0, stream>>>(a);
+        return launch_overlapped(rows_kernel<VEC, float>, dim3(blocks), kRowThreads, 0, stream, a);
+    if (dtype == FATHOM_BF16)
+        return launch_overlapped(rows_kernel<VEC, __nv_bfloat16>, dim3(blocks), kRowThreads, 0, stream, a);
+    return launch_overlapped(rows_kernel<VEC, __half>, dim3(blocks), kRowThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -401,12 +402,9 @@ cudaError_t launch_rows(RowsArgs a, int dtype, bool vector, cudaStream_t stream)
     }
     if (blocks[0] + blocks[1] > INT32_MAX) return cudaErrorInvalidValue;
     a.blocks0 = (int)blocks[0];
-    if (vector)
-        launch_rows_vec<8>(a, dtype, (int)(blocks[0] + blocks[1]), stream);
-    else
-        launch_rows_vec<1>(a, dtype, (int)(blocks[0] + blocks[1]), stream);
     note_launch();
-    return cudaGetLastError();
+    return vector ? launch_rows_vec<8>(a, dtype, (int)(blocks[0] + blocks[1]), stream)
+                  : launch_rows_vec<1>(a, dtype, (int)(blocks[0] + blocks[1]), stream);
 }
 
 }  // namespace fathom
