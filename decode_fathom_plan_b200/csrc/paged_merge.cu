@@ -3,7 +3,7 @@
 // Part p of a row holds a_p = sum_j 2^(s_j - m_p) V_j and l_p = sum_j
 // 2^(s_j - m_p); the row is sum_p 2^(m_p - M) a_p / sum_p 2^(m_p - M) l_p with
 // M = max m_p.  One CTA per row: d/4 lanes of 16-byte loads by as many part
-// groups as fit, each with a running maximum over four parts at a time, so
+// groups as fit, each with a running maximum over several parts at a time, so
 // that a row of 32 parts costs one round of loads; the groups are summed
 // through shared memory in a fixed order.
 // It is launched while the kernels before it run (programmatic dependent
@@ -15,13 +15,16 @@
 namespace fathom {
 namespace {
 
-constexpr int kMergeThreads = 256;
-constexpr int kAtOnce = 4;
+// Few rows: threads for their parts.  Many: small CTAs, which wait beside the kernel before them
+// without taking its room (16 sessions 76.4 us a call, with 256 threads 78.3), but 92 places of 460
+// rows cost 24.0 us a call with 128 threads and 23.0 with 256.
+constexpr int kFewRows = 148 * 4, kFewThreads = 256, kManyThreads = 128;
 
-template <typename T>
+template <typename T, int kMergeThreads>
 __global__ void __launch_bounds__(kMergeThreads)
 merge_parts_kernel(const MergeArgs a)
 {
+    constexpr int kAtOnce = kMergeThreads == kManyThreads ? 8 : 6;
     __shared__ float4 s_o[kMergeThreads];
     __shared__ float s_m[kMergeThreads], s_l[kMergeThreads];
     const int row = blockIdx.x, b = row / a.n_heads, head = row - b * a.n_heads;
@@ -146,9 +149,14 @@ cudaError_t launch_merge_parts(const MergeArgs &args, int dtype, cudaStream_t st
     a.status = device_status_ptr();
     note_launch();
     const int rows = a.q.n_seqs * a.n_heads;
-    return dtype == FATHOM_BF16
-               ? launch_overlapped(merge_parts_kernel<__nv_bfloat16>, dim3(rows), kMergeThreads, 0, stream, a)
-               : launch_overlapped(merge_parts_kernel<__half>, dim3(rows), kMergeThreads, 0, stream, a);
+    const auto go = [&](auto kernel, int threads) {
+        return launch_overlapped(kernel, dim3(rows), threads, 0, stream, a);
+    };
+    if (dtype == FATHOM_BF16)
+        return rows <= kFewRows ? go(merge_parts_kernel<__nv_bfloat16, kFewThreads>, kFewThreads)
+                                : go(merge_parts_kernel<__nv_bfloat16, kManyThreads>, kManyThreads);
+    return rows <= kFewRows ? go(merge_parts_kernel<__half, kFewThreads>, kFewThreads)
+                            : go(merge_parts_kernel<__half, kManyThreads>, kManyThreads);
 }
 
 }  // namespace fathom
