@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kMaxHeads = 65535;      // also the y and z extent of a grid
 constexpr int kMaxSequences = 65535;
+constexpr int kMaxList = 1 << 28;     // listed keys of a query
 
 fathom_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FATHOM_OK : FATHOM_ERR_CUDA; }
 
@@ -278,7 +279,7 @@ size_t fathom_sparse_attention_paged_workspace_bytes(int32_t n_seqs, int32_t n_h
                                                      int32_t head_dim, int32_t k)
 {
     if (n_seqs < 1 || n_seqs > kMaxSequences || n_heads < 1 || n_heads > kMaxHeads || k < 1 ||
-        !head_dim_ok(head_dim) || (long long)n_seqs * n_heads >= (1ll << 31))
+        k > kMaxList || !head_dim_ok(head_dim) || (long long)n_seqs * n_heads >= (1ll << 31))
         return 0;
     return paged_sparse_bytes(n_seqs * n_heads, head_dim, k);
 }
@@ -292,7 +293,7 @@ fathom_status fathom_sparse_attention_paged(const fathom_kv_cache *cache, const 
                                             size_t workspace_bytes, cudaStream_t stream)
 {
     NvtxRange range("fathom_sparse_attention_paged");
-    if (!cache_ok(cache) || !page_table || !seq_lens || !idx || k < 1 || table_stride < 1)
+    if (!cache_ok(cache) || !page_table || !seq_lens || !idx || k < 1 || k > kMaxList || table_stride < 1)
         return FATHOM_ERR_INVALID_ARG;
     const int group = query_group(cache, q, out, n_seqs, softmax_scale, softcap);
     if (!group) return FATHOM_ERR_INVALID_ARG;

@@ -158,6 +158,17 @@ __device__ __forceinline__ int angle_slot(int which, int u, int j, int units)
 {
     return VEC == 8 ? ((which * 2 + (j >> 2)) * units + u) * 4 + (j & 3) : which * units + u;
 }
+// The four of a 16-byte word, or one.
+template <int VEC>
+__device__ __forceinline__ void angles(const float *from, float *to)
+{
+    if constexpr (VEC == 8) {
+        const float4 v = *reinterpret_cast<const float4 *>(from);
+        to[0] = v.x; to[1] = v.y; to[2] = v.z; to[3] = v.w;
+    } else {
+        to[0] = from[0];
+    }
+}
 // Fraction of a turn in units of 2^-64.
 __device__ __forceinline__ unsigned long long turn_fraction(double turns)
 {
@@ -340,9 +351,9 @@ rows_kernel(const RowsArgs a)
             if (u < rot_units) {
                 float c[VEC], s[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    c[j] = cs[angle_slot<VEC>(0, u, j, rot_units)];
-                    s[j] = cs[angle_slot<VEC>(1, u, j, rot_units)];
+                for (int j = 0; j < VEC; j += VEC == 8 ? 4 : 1) {
+                    angles<VEC>(cs + angle_slot<VEC>(0, u, j, rot_units), c + j);
+                    angles<VEC>(cs + angle_slot<VEC>(1, u, j, rot_units), s + j);
                 }
                 if constexpr (VEC == 1) {
                     rotate(lo[i][0], hi[i][0], c[0], s[0]);

@@ -390,7 +390,10 @@ fathom_status fathom_sparse_attention(const float *keys, const float *values, in
  * keys and values into the pages, fathom_sparse_attention_paged attends over
  * the keys that fathom_scan_topk selected, and fathom_paged_attention over
  * every key of a sequence.  All are stream-ordered, may be captured in a
- * CUDA graph, allocate nothing and make no host synchronisation. */
+ * CUDA graph (make the first call of a kind, which may load its device code,
+ * before a capture), allocate nothing and make no host synchronisation.  Their
+ * kernels are launched while the kernel before them in the stream ends
+ * (programmatic stream serialization) and touch no memory before it has. */
 
 /* Element types of rows and caches. */
 typedef enum {
@@ -530,10 +533,11 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  * [n_seqs]) may change between replays of a captured call; max_len is the
  * host's bound on them.  A length that is negative, above max_len or, if not
  * 0, below prefix_len sets FATHOM_ERR_INVALID_ARG in the device status, and
- * that sequence gets zeros.  A key on a bad page is skipped (one of the
- * prefix takes part with a K and V of zeros).
+ * that sequence gets zeros.  A key on a bad page is skipped (one of a shared
+ * prefix may take part with a K and V of zeros instead).
  * q, out: rows of n_seqs tokens with G*n_kv_heads heads, in the cache's type,
- * 16-byte aligned, strides positive multiples of 8; G 1..8.  slopes: device float32
+ * 16-byte aligned, strides positive multiples of 8, n_seqs at most 65535; G
+ * 1..8.  slopes: device float32
  * [G*n_kv_heads].  Scores, softmax and sums are float32; each probability is
  * rounded to the cache's type for its product with V, which is accumulated in
  * float32.  workspace: device memory that no other call in flight uses. */
@@ -558,7 +562,7 @@ size_t fathom_sparse_attention_paged_workspace_bytes(int32_t n_seqs, int32_t n_h
  * sets FATHOM_ERR_INVALID_ARG in the device status.  k and v of the cache may
  * be pinned host memory: only the listed rows cross the link.  q, out, slopes
  * and workspace as for fathom_paged_attention; all arithmetic is float32,
- * with one rounding of the output. */
+ * with one rounding of the output.  k at most 2^28. */
 fathom_status fathom_sparse_attention_paged(const fathom_kv_cache *cache, const fathom_rows *q,
                                             const int32_t *idx, int32_t k,
                                             const int32_t *page_table, int32_t table_stride,

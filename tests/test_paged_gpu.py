@@ -94,6 +94,20 @@ def test_norm_rope_unaligned_rows_in_place_and_one_sided(shift):
     assert (base[:shift] == 0).all() and (base[shift + T * h * d:] == 0).all()
 
 
+def test_norm_rope_of_positions_below_zero_and_at_the_end_of_the_range():
+    pos = torch.tensor([-1, -7, -2 ** 31, 2 ** 31 - 1, 0, 1 << 24], dtype=torch.int32, device="cuda")
+    for d, inter in ((128, False), (96, True)):
+        x = randn([6, 2, d], F32, 4).cuda()
+        guard = torch.full([6 * 2 * d + 64], 7.0, device="cuda")
+        out = guard[:6 * 2 * d].view(6, 2, d)
+        fp.fathom_qk_norm_rope(x, None, pos, out, None, fp.RotaryTable(d, base=1e6, interleaved=inter))
+        p = pos.cpu().numpy().astype(np.float64)
+        y, size = po.norm_rope(po.f64(x), p, None, 1e-6, po.turns(d, 1e6)[0], 1.0, inter)
+        # the reference's own angle is a float64 product of some 2^31 radians: 2^-22 of a radian
+        check(out, y, po.norm_rope_tolerance(y, size, F32) + 2.0 ** -21 * size)
+        assert (guard[6 * 2 * d:] == 7.0).all()
+
+
 def test_norm_rope_without_rotation_or_norm():
     x = randn([4, 2, 96], F16, 1).cuda()
     out = torch.empty([4, 2, 96], dtype=F32, device="cuda")
@@ -560,6 +574,25 @@ def test_attention_strided_rows_and_offsets_past_32_bits():
                                      b.lens_t, out, ws, b.scale)
     check(out, want, tol)
     assert status() == fp.FATHOM_OK
+
+
+def test_attention_refuses_a_cache_in_host_memory():
+    b = Batch([100], 0, 1, 2, 64, 16, BF16, False, 4, residency="host_mapped")
+    with pytest.raises(fp.FathomError) as e:
+        b.attention()
+    assert e.value.status == fp.FATHOM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("prefix", [0, 2048])
+def test_attention_writes_only_its_output_rows(prefix):
+    b = Batch([prefix + 70, 0, prefix + 1], prefix, 8, 2, 96, 16, F16, False, 4)
+    wide = torch.full([3, 18, 104], 5.0, dtype=F16, device="cuda")
+    b.out = wide[:, 1:17, :96]
+    b.attention()
+    want, tol = b.expect()
+    check(b.out, want, tol)
+    b.out.fill_(5.0)
+    assert (wide == 5.0).all()
 
 
 def test_attention_workspace_too_small_is_refused():
