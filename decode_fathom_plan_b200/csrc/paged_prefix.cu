@@ -297,9 +297,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     const uint32_t o_col = kSlots * kTile;                      // O of slot s at o_col + s*d
 
     if (warp == 0) {
-        // a stage that both slots read is freed by both; P comes from four warps
+        // a stage is freed by both slots, whether they read it or not; P comes from four warps
         for (int i = lane; i < kBarriers; i += 32)
-            mbar_init(bar(i), i >= kEmpty && i < kScores ? (shared ? kSlots : 1) : i >= kProbs && i < kDone ? 4 : 1);
+            mbar_init(bar(i), i >= kEmpty && i < kScores ? kSlots : i >= kProbs && i < kDone ? 4 : 1);
         if (lane == 0) s_stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -410,12 +410,17 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             Place<kStages> at;
             int k = 0, v = 0;                                   // stages of the tiles in use
             bool ok = mbar_wait(bar(kQueries), 0, stop);
-            const auto take = [&](bool mine, int &stage) {
-                if (mine) {
-                    stage = at.stage;
-                    ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop);
-                }
+            const auto take = [&](int &stage) {
+                stage = at.stage;
+                ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop);
                 at.next();
+            };
+            // The other slot's tile is passed on: seen full and freed.  A warp that left such phases
+            // out could come back to a stage two of them early, which their parity does not show.
+            const auto pass = [&](const Place<kStages> &of) {
+                ok = ok && mbar_wait(bar(kFull + of.stage), of.phase, stop);
+                if (ok && elect_one()) mbar_arrive(bar(kEmpty + of.stage));
+                __syncwarp();
             };
             // S = Q K^T of step j, by one lane
             const auto scores = [&](int j) {
@@ -427,8 +432,15 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 }
                 umma_commit(bar(kScores + 2 * me + (j & 1)));
             };
-            for (int s = 0; s < takers; ++s)
-                if (walk.steps(s) > 0) take(shared || s == me, k);
+            for (int s = 0; s < takers; ++s) {
+                if (walk.steps(s) == 0) continue;
+                if (shared || s == me) {
+                    take(k);
+                } else {
+                    pass(at);
+                    at.next();
+                }
+            }
             tc_after();
             if (ok && steps > 0 && elect_one()) {
                 scores(0);
@@ -436,30 +448,47 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 umma_commit(bar(kEmpty + k));
             }
             __syncwarp();
-            for (int j = 0; j < steps && ok; ++j) {
+            for (int j = 0; j < walk.steps(0) && ok; ++j) {
                 const bool more = j + 2 < steps;
+                Place<kStages> others[2];                       // of V and K, passed on when this step is out
+                int n_others = 0;
                 if (!(j & 1))
                     for (int s = 0; s < takers; ++s) {
-                        if (j < walk.steps(s)) take(shared || s == me, v);
-                        if (j + 2 < walk.steps(s)) take(shared || s == me, k);
-                    }
-                const uint64_t v_desc = v_ring + v * kStageStep + (j & 1) * kHalfStep;
-                ok = ok && mbar_wait(bar(kProbs + 2 * me + (j & 1)), (j >> 1) & 1, stop);
-                tc_after();
-                if (ok && elect_one()) {
-                    // O += P V of step j; then S of step j + 2 goes where P was
+                        const bool has[2] = {j < walk.steps(s), j + 2 < walk.steps(s)};
+                        if (shared || s == me) {
+                            if (has[0]) take(v);
+                            if (has[1]) take(k);
+                        } else {
 #pragma unroll
-                    for (int x = 0; x < kStep / 16; ++x)        // 16 keys: 2048 bytes of V, 8 columns of P
-                        umma_ts(o_at, s_col + (j & 1) * kStep + x * 8, v_desc + x * (2048 >> 4), idesc_pv,
-                                j > 0 || x > 0);
-                    umma_commit(bar(kDone + 2 * me + (j & 1)));
-                    if (j & 1) umma_commit(bar(kEmpty + v));
-                    if (more) {
-                        scores(j + 2);
-                        if (j & 1) umma_commit(bar(kEmpty + k));
+                            for (int x = 0; x < 2; ++x)
+                                if (has[x]) {
+                                    others[x] = at;
+                                    n_others = x + 1;
+                                    at.next();
+                                }
+                        }
                     }
+                if (j < steps) {
+                    const uint64_t v_desc = v_ring + v * kStageStep + (j & 1) * kHalfStep;
+                    ok = ok && mbar_wait(bar(kProbs + 2 * me + (j & 1)), (j >> 1) & 1, stop);
+                    tc_after();
+                    if (ok && elect_one()) {
+                        // O += P V of step j; then S of step j + 2 goes where P was
+#pragma unroll
+                        for (int x = 0; x < kStep / 16; ++x)    // 16 keys: 2048 bytes of V, 8 columns of P
+                            umma_ts(o_at, s_col + (j & 1) * kStep + x * 8, v_desc + x * (2048 >> 4), idesc_pv,
+                                    j > 0 || x > 0);
+                        umma_commit(bar(kDone + 2 * me + (j & 1)));
+                        if (j & 1) umma_commit(bar(kEmpty + v));
+                        if (more) {
+                            scores(j + 2);
+                            if (j & 1) umma_commit(bar(kEmpty + k));
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (n_others > 0) pass(others[0]);
+                if (n_others > 1) pass(others[1]);
             }
             if (!ok) {                                          // let the products end
                 if (elect_one()) umma_commit(bar(kDrained + me));
