@@ -333,9 +333,15 @@ paged_split_kernel(const SplitArgs a)
                 for (int x = 0; x < 4; ++x) {
                     const float ref = m[x & 1] == -INFINITY ? 0.0f : m[x & 1];
                     p[x] = exp2_fast(c[u][x] - ref);
-                    l[x & 1] += p[x];
+                    if (kSplitP) l[x & 1] += p[x];
                 }
                 const uint32_t p0 = narrow2<T>(p[0], p[1]), p1 = narrow2<T>(p[2], p[3]);
+                if constexpr (!kSplitP) {
+                    // the sum of the rounded ones, those that V is weighted with
+                    const float2 w0 = widen2<T>(p0), w1 = widen2<T>(p1);
+                    l[0] += w0.x + w1.x;
+                    l[1] += w0.y + w1.y;
+                }
                 const uint32_t f0 = transpose8x8(p0), f1 = transpose8x8(p1);
                 uint32_t r0 = 0u, r1 = 0u;
                 if constexpr (kSplitP) {

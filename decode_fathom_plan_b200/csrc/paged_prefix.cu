@@ -570,10 +570,11 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 for (int k = 0; k < kStep; k += 2) {
                     float p0, p1;
                     fma2(Pair(x[k], x[k + 1]), mult2, ref2).split(p0, p1);
-                    p0 = exp2_fast(p0);
-                    p1 = exp2_fast(p1);
-                    sum[(k >> 1) & 3] = sum[(k >> 1) & 3] + Pair(p0, p1);
-                    p[k >> 1] = narrow2<T>(p0, p1);
+                    // the sum is of the rounded probabilities, those that V is weighted with: where few
+                    // keys have most of the weight, their rounding then cancels
+                    p[k >> 1] = narrow2<T>(exp2_fast(p0), exp2_fast(p1));
+                    const float2 w = widen2<T>(p[k >> 1]);
+                    sum[(k >> 1) & 3] = sum[(k >> 1) & 3] + Pair(w.x, w.y);
                 }
                 tmem_st32(s_addr, reinterpret_cast<const float *>(p));
                 {

@@ -392,6 +392,22 @@ def test_shared_prefix(lens, prefix, H, G, d, page, dtype, tm, cap, slopes):
         assert status() == fp.FATHOM_OK
 
 
+@pytest.mark.parametrize("page", [16, 128])
+def test_shared_prefix_beside_many_own_keys(page):
+    """Slots of a CTA that run apart from each other: the sums of every call are those of the first."""
+    b = Batch([20000 + 4000 - 17 * i for i in range(15)], 20000 // page * page, 3, 2, 128, page, BF16, False, 77)
+    b.attention()
+    check_rows(b, few_rows(b, 6))
+    first = b.out.clone()
+    for _ in range(300):
+        outs = []
+        for _ in range(8):
+            b.attention(ws=b.ws)
+            outs.append(b.out.clone())
+        assert all(torch.equal(o, first) for o in outs)
+    assert status() == fp.FATHOM_OK
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("G,d", [(1, 128), (4, 64), (2, 256)])
 def test_shared_prefix_of_growing_scores(dtype, G, d):
