@@ -490,8 +490,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                         for (int x = 0; x < kStep / 16; ++x)    // 16 keys: 2048 bytes of V, 8 columns of P
                             umma_ts(o_at, s_col + (j & 1) * kStep + x * 8, v_desc + x * (2048 >> 4), idesc_pv,
                                     j > 0 || x > 0);
-                        umma_commit(bar(kDone + 2 * me + (j & 1)));
+                        // the last one's sums are what the CTA ends with: nothing arrives after that
                         if (j & 1) umma_commit(bar(kEmpty + v));
+                        umma_commit(bar(kDone + 2 * me + (j & 1)));
                         if (more) {
                             scores(j + 2);
                             if (j & 1) umma_commit(bar(kEmpty + k));
