@@ -44,8 +44,10 @@ bool rotary_ok(const fathom_rotary *r, int head_dim)
            (r->interleaved == 0 || r->interleaved == 1) && isfinite(r->magnitude);
 }
 
-// A stride over n > 1 rows that are read or written 16 bytes at a time.
-bool stride_ok(int64_t stride, int n) { return n == 1 || (stride > 0 && stride % 8 == 0); }
+// A stride over n > 1 rows that are read or written in words of up to `words` elements.
+bool stride_ok(int64_t stride, int n, int words) { return n == 1 || (stride > 0 && stride % words == 0); }
+// The rows of a cache are read in words of 32 bytes.
+constexpr int kCacheWord = 16;
 
 bool cache_ok(const fathom_kv_cache *c)
 {
@@ -53,8 +55,9 @@ bool cache_ok(const fathom_kv_cache *c)
            (c->page_size & (c->page_size - 1)) == 0 && c->n_kv_heads >= 1 &&
            c->n_kv_heads <= kMaxHeads && head_dim_ok(c->head_dim) &&
            (c->dtype == FATHOM_BF16 || c->dtype == FATHOM_F16) &&
-           stride_ok(c->page_stride, c->n_pages) && stride_ok(c->head_stride, c->n_kv_heads) &&
-           stride_ok(c->token_stride, c->page_size);
+           stride_ok(c->page_stride, c->n_pages, kCacheWord) &&
+           stride_ok(c->head_stride, c->n_kv_heads, kCacheWord) &&
+           stride_ok(c->token_stride, c->page_size, kCacheWord);
 }
 
 int log2_of(int x)
@@ -68,7 +71,7 @@ int log2_of(int x)
 // pinned host memory through its device mapping where host_ok.
 fathom_status resolve_cache(void *p, bool host_ok, void **out)
 {
-    if (!p || !aligned16(p)) return FATHOM_ERR_INVALID_ARG;
+    if (!p || reinterpret_cast<uintptr_t>(p) % (2 * kCacheWord)) return FATHOM_ERR_INVALID_ARG;
     cudaPointerAttributes attr{};
     if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
         cudaGetLastError();
@@ -113,7 +116,7 @@ int query_group(const fathom_kv_cache *c, const fathom_rows *q, const fathom_row
     if (!rows_ok(q, n_seqs) || !rows_ok(out, n_seqs) || q->dtype != c->dtype || out->dtype != c->dtype) return 0;
     if (!aligned16(q->data) || !aligned16(out->data) || q->n_heads != out->n_heads) return 0;
     for (const fathom_rows *r : {q, out})
-        if (!stride_ok(r->token_stride, n_seqs) || !stride_ok(r->head_stride, r->n_heads)) return 0;
+        if (!stride_ok(r->token_stride, n_seqs, 8) || !stride_ok(r->head_stride, r->n_heads, 8)) return 0;
     if (q->n_heads % c->n_kv_heads || q->n_heads / c->n_kv_heads > kMaxGroup) return 0;
     if (n_seqs < 1 || n_seqs > kMaxSequences || (long long)n_seqs * q->n_heads >= (1ll << 31)) return 0;
     if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return 0;

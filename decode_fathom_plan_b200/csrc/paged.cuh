@@ -73,6 +73,35 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
     return r;
 }
 
+// --------------------------------------------------------------- cached rows
+// 32 bytes of a cached row: four lanes bring a whole line of 128 bytes with one instruction, where
+// 16 bytes a lane took two.
+__device__ __forceinline__ void load32(const void *p, bool there, uint4 &a, uint4 &b)
+{
+    a = b = make_uint4(0u, 0u, 0u, 0u);
+    if (there)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p));
+}
+// First of the eight channels that lane t of the four that share a key holds as its m-th group, of
+// E: 16 neighbours of every 64, and of a 32 left over 8.
+template <int E>
+__host__ __device__ __forceinline__ constexpr int group_channel(int m, int t)
+{
+    return m < (E & ~1) ? 64 * (m >> 1) + 16 * t + 8 * (m & 1) : 32 * (E - 1) + 8 * t;
+}
+// All of them of one row, from its first channel.
+template <int E>
+__device__ __forceinline__ void load_groups(const uint16_t *row, int t, bool there, uint4 (&to)[E])
+{
+#pragma unroll
+    for (int m = 0; m + 1 < E; m += 2) load32(row + group_channel<E>(m, t), there, to[m], to[m + 1]);
+    if constexpr (E & 1)
+        to[E - 1] = there ? __ldg(reinterpret_cast<const uint4 *>(row + group_channel<E>(E - 1, t)))
+                          : make_uint4(0u, 0u, 0u, 0u);
+}
+
 // -------------------------------------------------------------------- scores
 // 2^x, within 2^-22 of the value; 2^-inf = 0.
 __device__ __forceinline__ float exp2_fast(float x)

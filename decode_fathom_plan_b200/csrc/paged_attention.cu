@@ -8,14 +8,17 @@
 //   O^T [d x 8]      += V^T [d x 16 keys] P^T [16 keys x 8].
 // Both products contract or list the channels in an order that is free as
 // long as both operands, or the output, follow it.  It is chosen so that the
-// fragments of K and V are what 16-byte loads of the cached rows bring:
-//  - K: lane (g, t) = (lane/4, lane%4) loads channels [32j + 8t, +8) of keys g
-//    and g + 8; the four words are the A fragments of two k-steps whose
-//    contraction index (2t, 2t+1, 2t+8, 2t+9) stands for channels 32j + 8t +
-//    (4s..4s+3).  Q's fragments are loaded with the same indexes.
-//  - V: lane (g, t) loads channels [64j + 8g, +8) of keys 2t, 2t+1, 2t+8,
-//    2t+9; a byte permute pairs two keys' values of one channel, and the four
-//    m-tiles of the block take the channel pairs (8g + 2i, 8g + 2i + 1).
+// fragments of K and V are what 32-byte loads of the cached rows bring:
+//  - K: lane (g, t) = (lane/4, lane%4) loads channels [64j + 16t, +16) of keys
+//    g and g + 8; each four words are the A fragments of two k-steps whose
+//    contraction index (2t, 2t+1, 2t+8, 2t+9) stands for four neighbours of
+//    those channels.  Q's fragments are loaded with the same indexes.
+//  - V: lane (g, t) loads channels [128j + 16g, +16) of keys 2t, 2t+1, 2t+8,
+//    2t+9; a byte permute pairs two keys' values of one channel, and the eight
+//    m-tiles of the block take the channel pairs (16g + 2i, 16g + 2i + 1).
+//    What is left of a row whose length is no multiple of 64 or 128 takes shorter
+//    loads.  Against 16 bytes a lane: 64 agents' own keys 134.2 -> 131.8 us
+//    with the prefix, 16 sessions 76.5 -> 76.3, 4 x 8192 keys 29.1 -> 28.7.
 //  - P: the accumulator of S^T holds (key g; queries 2t, 2t+1), the B fragment
 //    wants (keys 2t, 2t+1; query g): an 8x8 transpose (movmatrix).
 // So nothing passes through shared memory before the end, every warp runs on
@@ -86,6 +89,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 
 constexpr int kUnitKeys = kSplitWarps * kBlockKeys;
 
+// First of the channel pair that lane group g has of m-tile i of O^T: 16
+// neighbours of every 128, then 8 of a 64 and 4 of a 32 left over.
+template <int E>
+__device__ __forceinline__ constexpr int tile_channel(int i, int g)
+{
+    if (i < 8 * (E / 4)) return 128 * (i >> 3) + 16 * g + 2 * (i & 7);
+    i -= 8 * (E / 4);
+    if ((E & 2) && i < 4) return 128 * (E / 4) + 8 * g + 2 * i;
+    return 32 * (E - 1) + 4 * g + 2 * (i & 3);
+}
+
 // A 16-byte load from shared memory that stays where it is written.
 __device__ __forceinline__ uint4 load_shared(const uint4 *p)
 {
@@ -131,7 +145,7 @@ paged_split_kernel(const SplitArgs a)
     constexpr int d = 32 * E;
     constexpr int kTilesM = d / 16;                 // m-tiles of O^T
     constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int kWordsV = (E / 2) * 4 + (E & 1) * 2;
+    constexpr int kWordsV = 2 * E;
     // What a warp loads at a time, 4 KB or more, must fit the registers with the accumulators: wide
     // heads keep Q's fragments (the same for every warp) in shared memory, narrow ones take
     // several blocks of keys.
@@ -211,10 +225,11 @@ paged_split_kernel(const SplitArgs a)
         uint4 qr[kSharedQ ? 1 : E];
         __syncthreads();                            // the last run's, and its outputs, are read
         if (!kSharedQ || warp == 0) {
-            const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + (h * G + g) * a.q.q_hs + 8 * t;
+            const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + (h * G + g) * a.q.q_hs;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const uint4 w4 = g < G ? *reinterpret_cast<const uint4 *>(q + 32 * e) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 w4 = g < G ? *reinterpret_cast<const uint4 *>(q + group_channel<E>(e, t))
+                                       : make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (kSharedQ)
                     s_q[e][lane] = w4;
                 else
@@ -229,8 +244,8 @@ paged_split_kernel(const SplitArgs a)
         }
         const int32_t *table = a.kv.table + (size_t)b * a.kv.table_stride;
         const int shift = a.kv.page_shift, mask = (1 << shift) - 1;
-        const T *K = static_cast<const T *>(a.kv.k) + h * a.kv.head_stride;
-        const T *V = static_cast<const T *>(a.kv.v) + h * a.kv.head_stride;
+        const uint16_t *K = static_cast<const uint16_t *>(a.kv.k) + h * a.kv.head_stride;
+        const uint16_t *V = static_cast<const uint16_t *>(a.kv.v) + h * a.kv.head_stride;
 
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         float o[kTilesM][4];
@@ -267,29 +282,32 @@ paged_split_kernel(const SplitArgs a)
                     bad |= j < hi && !ok;
                     at[x] = ok ? next[u][x] * a.kv.page_stride + (j & mask) * a.kv.slot_stride : -1;
                     key[u][x] = ok && j + g < hi;
-                    const T *p = K + at[x] + g * a.kv.slot_stride + 8 * t;
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        kr[u][x][e] = key[u][x] ? __ldg(reinterpret_cast<const uint4 *>(p + 32 * e))
-                                                : make_uint4(0u, 0u, 0u, 0u);
+                    load_groups<E>(K + at[x] + g * a.kv.slot_stride, t, key[u][x], kr[u][x]);
                 }
                 // keys past the end are not read: what their slots hold may be anything, NaN too
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int s = 2 * t + (x & 1);
                     const bool live = at[x >> 1] >= 0 && j0 + 8 * (x >> 1) + s < hi;
-                    const T *p = V + at[x >> 1] + s * a.kv.slot_stride;
+                    const uint16_t *p = V + at[x >> 1] + s * a.kv.slot_stride;
                     uint32_t *to = vr[u][x];
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        const uint4 w4 = live ? __ldg(reinterpret_cast<const uint4 *>(p + 64 * e + 8 * g))
+                    for (int e = 0; e < E / 4; ++e, to += 8) {
+                        uint4 v0, v1;
+                        load32(p + 128 * e + 16 * g, live, v0, v1);
+                        to[0] = v0.x; to[1] = v0.y; to[2] = v0.z; to[3] = v0.w;
+                        to[4] = v1.x; to[5] = v1.y; to[6] = v1.z; to[7] = v1.w;
+                    }
+                    if constexpr (E & 2) {
+                        const uint4 w4 = live ? __ldg(reinterpret_cast<const uint4 *>(p + 128 * (E / 4) + 8 * g))
                                               : make_uint4(0u, 0u, 0u, 0u);
-                        to[4 * e] = w4.x; to[4 * e + 1] = w4.y; to[4 * e + 2] = w4.z; to[4 * e + 3] = w4.w;
+                        to[0] = w4.x; to[1] = w4.y; to[2] = w4.z; to[3] = w4.w;
+                        to += 4;
                     }
                     if constexpr (E & 1) {
                         const uint2 w2 = live ? __ldg(reinterpret_cast<const uint2 *>(p + 32 * (E - 1) + 4 * g))
                                               : make_uint2(0u, 0u);
-                        to[kWordsV - 2] = w2.x; to[kWordsV - 1] = w2.y;
+                        to[0] = w2.x; to[1] = w2.y;
                     }
                 }
             }
@@ -378,8 +396,7 @@ paged_split_kernel(const SplitArgs a)
             }
 #pragma unroll
             for (int i = 0; i < kTilesM; ++i) {
-                const int c0 = i < 4 * (E / 2) ? 64 * (i >> 2) + 8 * g + 2 * (i & 3)
-                                               : 32 * (E - 1) + 4 * g + 2 * (i & 3);
+                const int c0 = tile_channel<E>(i, g);
                 *reinterpret_cast<float2 *>(&s_o[warp][2 * t + x][c0]) = make_float2(o[i][x], o[i][x + 2]);
             }
         }

@@ -5,16 +5,16 @@
 //
 // Every list is its query's own, so a key row serves one query: 4*d flops for
 // 4*d bytes of K and V, and only the reads count.  Four lanes share a key,
-// lane t holding channels [32j + 8t, +8), so a 16-byte load of each brings 64
-// bytes of the row, a warp has eight keys at once, a dot product costs two
-// shuffles, and the sums over V need none: each group of four lanes keeps its
+// lane t holding channels [64j + 16t, +16), so a 32-byte load of each brings a
+// line of the row (16-byte loads: 10.9 us for 10.6 in the second case below),
+// a warp has eight keys at once, a dot product costs two shuffles, and the sums over V need none: each group of four lanes keeps its
 // own running maximum, sum and output, which are joined once at the end.
 // A query's list is split into runs, one CTA each.  Registers (the output and
 // the query: 48 of some 126 at d = 128) leave 16 warps of 4 KB in flight a
 // multiprocessor; a second step's rows on their way at 12 warps was slower.
 // Measured on B200: 512 rows of 1024 keys of 128 channels, lists of 16
 // sequences, 55 us (4.3 TB/s, 67% of a plain copy, of single 256-byte rows); 32 rows of
-// 2048 keys 11.8 us.
+// 2048 keys 10.6 us.
 #include <math.h>
 
 #include <algorithm>
@@ -54,8 +54,8 @@ paged_sparse_kernel(const SparseArgs a)
     const int32_t *table = a.kv.table + (size_t)b * a.kv.table_stride;
     const int32_t *idx = a.idx + ((size_t)b * n_heads + head) * a.k;
     const int shift = a.kv.page_shift, mask = (1 << shift) - 1;
-    const T *K = static_cast<const T *>(a.kv.k) + h * a.kv.head_stride + 8 * t;
-    const T *V = static_cast<const T *>(a.kv.v) + h * a.kv.head_stride + 8 * t;
+    const uint16_t *K = static_cast<const uint16_t *>(a.kv.k) + h * a.kv.head_stride;
+    const uint16_t *V = static_cast<const uint16_t *>(a.kv.v) + h * a.kv.head_stride;
     const float slope = a.q.slopes ? a.q.slopes[head] * kLog2e : 0.0f;
 
     // Offset of the listed key i, -1 where there is none.  A warp looks its keys up 32 at a time, a
@@ -77,9 +77,9 @@ paged_sparse_kernel(const SparseArgs a)
     int key_next = entry(i0 + lane), key_then = entry(i0 + kSparseWarps * 32 + lane);
     uint4 qr[E];
     {
-        const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + head * a.q.q_hs + 8 * t;
+        const T *q = static_cast<const T *>(a.q.q) + b * a.q.q_ts + head * a.q.q_hs;
 #pragma unroll
-        for (int j = 0; j < E; ++j) qr[j] = *reinterpret_cast<const uint4 *>(q + 32 * j);
+        for (int j = 0; j < E; ++j) qr[j] = *reinterpret_cast<const uint4 *>(q + group_channel<E>(j, t));
     }
     long long at_next = look_up(key_next);
     float m = -INFINITY, l = 0.0f, o[E][8];
@@ -100,14 +100,8 @@ paged_sparse_kernel(const SparseArgs a)
             const int key = __shfl_sync(0xFFFFFFFFu, key_of, from);
             const long long at = __shfl_sync(0xFFFFFFFFu, at_of, from);
             uint4 kr[E], vr[E];
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                kr[j] = vr[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (at >= 0) {
-                    kr[j] = __ldg(reinterpret_cast<const uint4 *>(K + at + 32 * j));
-                    vr[j] = __ldg(reinterpret_cast<const uint4 *>(V + at + 32 * j));
-                }
-            }
+            load_groups<E>(K + at, t, at >= 0, kr);
+            load_groups<E>(V + at, t, at >= 0, vr);
             float dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < E; ++j) {
@@ -169,7 +163,7 @@ paged_sparse_kernel(const SparseArgs a)
         for (int j = 0; j < E; ++j)
 #pragma unroll
             for (int x = 0; x < 8; x += 4)
-                *reinterpret_cast<float4 *>(&s_o[warp][32 * j + 8 * t + x]) =
+                *reinterpret_cast<float4 *>(&s_o[warp][group_channel<E>(j, t) + x]) =
                     make_float4(o[j][x], o[j][x + 1], o[j][x + 2], o[j][x + 3]);
         if (lane == 0) {
             s_m[warp] = top;

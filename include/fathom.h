@@ -476,7 +476,7 @@ fathom_status fathom_qk_norm_rope(int32_t n_tokens, int32_t head_dim, const int3
  * element p*page_stride + h*head_stride + s*token_stride + c of k (of v for
  * its value); strides in elements.  k and v: device memory, or pinned host
  * memory used through its device mapping (an offloaded cache; not for
- * fathom_paged_attention); 16-byte aligned, strides positive multiples of 8.
+ * fathom_paged_attention); 32-byte aligned, strides positive multiples of 16.
  * A page table is device int32 [n_seqs][table_stride]: key j of sequence b
  * lies in slot j % page_size of page page_table[b][j / page_size].
  * Sequences may share pages.  Entries behind a sequence's last key are never

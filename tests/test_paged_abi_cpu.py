@@ -91,7 +91,8 @@ def test_norm_rope_refusals(lib):
 BAD_CACHES = [dict(k=0), dict(v=0), dict(k=FAKE + 8), dict(page_size=4), dict(page_size=24),
               dict(page_size=2048), dict(n_pages=0), dict(n_kv_heads=0), dict(head_dim=48),
               dict(head_dim=288), dict(dtype=fp.FATHOM_F32), dict(page_stride=-8),
-              dict(token_stride=132), dict(head_stride=4)]
+              dict(token_stride=132), dict(head_stride=4), dict(token_stride=136), dict(k=FAKE + 16),
+              dict(v=FAKE + 16), dict(page_stride=8 * 128 * 16 + 8)]
 
 
 def append(lib, c=None, T=4, k=None, v=None, seq=FAKE, pos=FAKE, pt=FAKE, n=2, stride=8, rot=None,
