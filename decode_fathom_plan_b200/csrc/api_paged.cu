@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 using namespace fathom;
 
@@ -67,7 +68,7 @@ int log2_of(int x)
     return s;
 }
 
-// A device-usable address of a cache array: device or managed memory as is,
+// A device-usable address of a cache array: the current device's or managed memory as is,
 // pinned host memory through its device mapping where host_ok.
 fathom_status resolve_cache(void *p, bool host_ok, void **out)
 {
@@ -77,6 +78,9 @@ fathom_status resolve_cache(void *p, bool host_ok, void **out)
         cudaGetLastError();
         return FATHOM_ERR_INVALID_ARG;
     }
+    int device = 0;
+    if (attr.type == cudaMemoryTypeDevice && (cudaGetDevice(&device) != cudaSuccess || attr.device != device))
+        return FATHOM_ERR_INVALID_ARG;
     if (attr.type == cudaMemoryTypeDevice || attr.type == cudaMemoryTypeManaged) {
         *out = p;
         return FATHOM_OK;
@@ -119,7 +123,8 @@ int query_group(const fathom_kv_cache *c, const fathom_rows *q, const fathom_row
         if (!stride_ok(r->token_stride, n_seqs, 8) || !stride_ok(r->head_stride, r->n_heads, 8)) return 0;
     if (q->n_heads % c->n_kv_heads || q->n_heads / c->n_kv_heads > kMaxGroup) return 0;
     if (n_seqs < 1 || n_seqs > kMaxSequences || (long long)n_seqs * q->n_heads >= (1ll << 31)) return 0;
-    if (!isfinite(scale) || !isfinite(softcap) || softcap < 0.0f) return 0;
+    if (!(softcap >= 0.0f && softcap <= kMaxSoftcap)) return 0;
+    if (!isfinite(scale) || !isfinite(score_args(scale, softcap).scale)) return 0;
     return q->n_heads / c->n_kv_heads;
 }
 
@@ -266,13 +271,13 @@ fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_
         prefix_len % cache->page_size || table_stride < 1 ||
         (long long)table_stride * cache->page_size < max_len)
         return FATHOM_ERR_INVALID_ARG;
-    PagedView view{};
-    const fathom_status st = paged_view(cache, false, page_table, table_stride, &view);
-    if (st != FATHOM_OK) return st;
     const size_t need = paged_attention_bytes(cache->n_kv_heads, cache->head_dim, n_seqs, group,
                                               max_len, prefix_len);
     if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
         return FATHOM_ERR_WORKSPACE;
+    PagedView view{};
+    const fathom_status st = paged_view(cache, false, page_table, table_stride, &view);
+    if (st != FATHOM_OK) return st;
     return cuda_status(launch_paged_attention(
         view, paged_query(q, out, seq_lens, slopes, softmax_scale, softcap, n_seqs, group), max_len,
         prefix_len, workspace, stream));
@@ -300,12 +305,12 @@ fathom_status fathom_sparse_attention_paged(const fathom_kv_cache *cache, const 
         return FATHOM_ERR_INVALID_ARG;
     const int group = query_group(cache, q, out, n_seqs, softmax_scale, softcap);
     if (!group) return FATHOM_ERR_INVALID_ARG;
-    PagedView view{};
-    const fathom_status st = paged_view(cache, true, page_table, table_stride, &view);
-    if (st != FATHOM_OK) return st;
     const size_t need = paged_sparse_bytes(n_seqs * q->n_heads, cache->head_dim, k);
     if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
         return FATHOM_ERR_WORKSPACE;
+    PagedView view{};
+    const fathom_status st = paged_view(cache, true, page_table, table_stride, &view);
+    if (st != FATHOM_OK) return st;
     return cuda_status(launch_paged_sparse(
         view, paged_query(q, out, seq_lens, slopes, softmax_scale, softcap, n_seqs, group), idx, k,
         workspace, stream));

@@ -114,7 +114,10 @@ __device__ __forceinline__ float exp2_fast(float x)
 // A dot product as a logit times log2(e), so that the softmax is a power of
 // two.  The cap is cap * tanh(x / cap) with tanh(y) = 1 - 2 / (1 + e^2y): its
 // error is some 2^-23 of the cap, an absolute one of a logit; the hardware's
-// own tanh is 2^-11 off, 0.02 of a logit at a cap of 50.
+// own tanh is 2^-11 off, 0.02 of a logit at a cap of 50.  Larger caps than
+// kMaxSoftcap, where the error is 2^-8 of a logit at most (half a step of a
+// bfloat16 probability), are refused.
+constexpr float kMaxSoftcap = 16384.0f;
 struct ScoreArgs {
     float scale;      // softmax_scale * log2(e); with a cap 2 * log2(e) * softmax_scale / cap
     float cap;        // cap * log2(e), or 0 without a cap

@@ -474,9 +474,10 @@ fathom_status fathom_qk_norm_rope(int32_t n_tokens, int32_t head_dim, const int3
 
 /* A paged K/V cache: channel c of KV head h of the key in slot s of page p is
  * element p*page_stride + h*head_stride + s*token_stride + c of k (of v for
- * its value); strides in elements.  k and v: device memory, or pinned host
- * memory used through its device mapping (an offloaded cache; not for
- * fathom_paged_attention); 32-byte aligned, strides positive multiples of 16.
+ * its value); strides in elements.  k and v: memory of the current
+ * device, or pinned host memory used through its device mapping (an offloaded
+ * cache; not for fathom_paged_attention); 32-byte aligned, strides positive
+ * multiples of 16.
  * A page table is device int32 [n_seqs][table_stride]: key j of sequence b
  * lies in slot j % page_size of page page_table[b][j / page_size].
  * Sequences may share pages.  Entries behind a sequence's last key are never
@@ -521,7 +522,8 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
 /* Softmax attention of one query token per sequence over all its keys.  For
  * query head i = h*G + g of sequence b with n = seq_lens[b] keys,
  *   s_j = softmax_scale * (q[b][i] . K_j),
- *   s_j = softcap * tanh(s_j / softcap)     where softcap > 0,
+ *   s_j = softcap * tanh(s_j / softcap)     where softcap > 0 (at most 16384;
+ *                                           within 2^-22 * softcap),
  *   s_j = s_j - slopes[i] * (n - 1 - j)     where slopes is not NULL
  *                                           (the query stands at n - 1),
  *   out[b][i] = sum_j softmax(s)_j V_j,  j in [0, n).

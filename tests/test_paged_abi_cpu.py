@@ -148,6 +148,33 @@ def test_attention_refusals(lib):
         assert sparse(lib, **kw) == bad
 
 
+def test_attention_refusals_beside_a_call_that_lacks_only_its_workspace(lib):
+    bad, lacking = fp.FATHOM_ERR_INVALID_ARG, fp.FATHOM_ERR_WORKSPACE
+    for call, kw in ((attention, dict(max_len=1000)), (sparse, dict(k=4096))):
+        def at(**more):
+            return call(lib, **{**kw, "ws": 0, **more})
+        assert at() == lacking
+        for cap in (1e-30, 50.0, 16384.0):
+            assert at(cap=cap) == lacking
+        for cap in (-1e-30, 16385.0, 3e38, math.inf, math.nan, 1e-40):
+            assert at(cap=cap) == bad
+        for scale in (math.inf, math.nan, 3e38, -3e38):
+            assert at(scale=scale) == bad
+        for scale in (1e38, 0.0, -0.1):
+            assert at(scale=scale) == lacking
+        assert at(cap=1.0, scale=2e38) == bad
+        for c in (dict(token_stride=136), dict(head_stride=136), dict(page_stride=136), dict(head_dim=48)):
+            assert at(c=cache(**c)) == bad
+        for r in (dict(token_stride=4100), dict(head_stride=132), dict(data=FAKE + 8)):
+            assert at(q=rows(32, **r)) == bad and at(out=rows(32, **r)) == bad
+        for r in (dict(token_stride=4104), dict(head_stride=136), dict(data=FAKE + 16)):
+            assert at(q=rows(32, **r), out=rows(32, **r)) == lacking
+    c = cache()
+    assert fp.fathom_paged_attention_workspace_bytes(c, 2, 4, 1000) > 0
+    for kw in (dict(token_stride=136), dict(head_stride=136), dict(page_stride=136)):
+        assert fp.fathom_paged_attention_workspace_bytes(cache(**kw), 2, 4, 1000) == 0
+
+
 def test_workspace_sizes(lib):
     c = cache()
     size = fp.fathom_paged_attention_workspace_bytes

@@ -592,6 +592,30 @@ def test_attention_strided_rows_and_offsets_past_32_bits():
     assert status() == fp.FATHOM_OK
 
 
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 16384.0])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_smallest_and_largest_caps(cap, dtype):
+    """Bounds as everywhere: 2^-21 of the cap for a score."""
+    own = Batch([300, 5], 0, 2, 4, 64, 16, dtype, False, 11)
+    own.attention(cap=cap)
+    want, tol = own.expect(cap)
+    check(own.out, want, tol)
+    idx = np.full((2, 8, 300), -1, np.int32)
+    for b, n in enumerate(own.lens):
+        idx[b, :, :n] = np.arange(n)
+    need = fp.fathom_sparse_attention_paged_workspace_bytes(2, 8, 64, 300)
+    ws = torch.empty(max(16, need), dtype=torch.uint8, device="cuda")
+    fp.fathom_sparse_attention_paged(own.kv.desc, own.q, torch.from_numpy(idx).cuda(), own.table_t, own.lens_t,
+                                     own.out, ws, own.scale, cap)
+    want, tol = own.expect(cap, idx=idx, round_p=False)
+    check(own.out, want, tol)
+    shared = Batch([2048 + i for i in range(9)], 2048, 2, 4, 64, 16, dtype, False, 12)
+    assert 8 * 2048 * 2 * 64 * 4 >= 8 << 20
+    shared.attention(cap=cap)
+    check_rows(shared, {(0, 0), (3, 5), (8, 7)}, cap)
+    assert status() == fp.FATHOM_OK
+
+
 def test_attention_refuses_a_cache_in_host_memory():
     b = Batch([100], 0, 1, 2, 64, 16, BF16, False, 4, residency="host_mapped")
     with pytest.raises(fp.FathomError) as e:
