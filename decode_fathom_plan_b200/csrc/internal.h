@@ -225,7 +225,7 @@ struct PrefixPlan {
 PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int prefix_len);
 // Writes the first p.parts places of every row.
 cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const PrefixPlan &p,
-                                const PartsView &pv, int prefix_len, cudaStream_t stream);
+                                const PartsView &pv, int prefix_len, int max_len, cudaStream_t stream);
 
 // ---- scan.cu
 struct ScanSessionArgs {

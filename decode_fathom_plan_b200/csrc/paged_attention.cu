@@ -516,7 +516,7 @@ cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int
     a.info = reinterpret_cast<int2 *>(static_cast<unsigned char *>(ws) + parts_bytes(p.places, kv.head_dim));
     a.status = device_status_ptr();
     cudaError_t e = cudaSuccess;
-    if (p.prefix.parts) e = launch_paged_prefix(kv, q, p.prefix, a.pv, prefix_len, stream);
+    if (p.prefix.parts) e = launch_paged_prefix(kv, q, p.prefix, a.pv, prefix_len, max_len, stream);
     if (e == cudaSuccess && p.ctas) {
         e = kv.dtype == FATHOM_BF16 ? launch_split<__nv_bfloat16>(a, p.ctas, stream)
                                     : launch_split<__half>(a, p.ctas, stream);

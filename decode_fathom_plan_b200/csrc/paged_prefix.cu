@@ -72,7 +72,8 @@ struct PrefixArgs {
     PagedQuery q;
     PartsView pv;
     ScoreArgs score;
-    const int32_t *table;                        // the first row of the page table
+    const int32_t *table;
+    int table_stride, max_len;
     int n_heads, n_pages, page_shift, head_dim;
     int prefix_len, seqs, slot_seqs, split_tiles, split_rest, two_blocks, parts;
     int *status;
@@ -321,12 +322,25 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         const CUtensorMap *map = keys ? &kmap : &vmap;
         const int shift = a.page_shift, box = min(1 << shift, kTile);
         const int boxes = kTile / box;                          // per 64-channel block
-        // lane x: the page of box x of a tile, looked up a tile ahead
+        // lane x: the page of box x of a tile, looked up a tile ahead, in the row of the first
+        // sequence that takes part: the row of an empty one (a padded batch row) may hold anything
+        const int32_t *table = a.table;
         const auto page_of = [&](int tile) {
             const int key = (t0 + tile) * kTile + lane * box;
-            return lane < boxes && key < a.prefix_len ? a.table[key >> shift] : a.n_pages;
+            return lane < boxes && key < a.prefix_len ? table[key >> shift] : a.n_pages;
         };
-        int page = page_of(0);
+        int page = page_of(0);                                  // mostly that row: beside the lengths
+        int from = -1;
+        for (int s = 0; s < a.seqs && from < 0; s += 32) {
+            const int n = s + lane < a.seqs ? a.q.seq_lens[s + lane] : 0;
+            const unsigned in = __ballot_sync(0xFFFFFFFFu, n > 0 && !refused_length(n, a.prefix_len, a.max_len));
+            if (in) from = s + __ffs(in) - 1;
+        }
+        const int keys_end = from < 0 ? 0 : a.prefix_len;       // with no sequence, no page is looked at
+        if (from > 0) {
+            table += (size_t)from * a.table_stride;
+            page = page_of(0);
+        }
         __syncwarp();
         if (elect_one()) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -356,8 +370,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             if (ok && mine) ok = mbar_wait(bar(kEmpty + at.stage), at.phase ^ 1, stop);
             if (ok && mine) {
                 int p = page;
-                if (p < 0 || p > a.n_pages || (p == a.n_pages && lane < boxes &&
-                                               (t0 + tile) * kTile + lane * box < a.prefix_len)) {
+                if (lane >= boxes || (t0 + tile) * kTile + lane * box >= keys_end) {
+                    p = a.n_pages;
+                } else if (p < 0 || p >= a.n_pages) {
                     bad = true;
                     p = a.n_pages;
                 }
@@ -755,7 +770,7 @@ PrefixPlan plan_prefix(int n_kv_heads, int head_dim, int n_seqs, int group, int 
 }
 
 cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const PrefixPlan &p,
-                                const PartsView &pv, int prefix_len, cudaStream_t stream)
+                                const PartsView &pv, int prefix_len, int max_len, cudaStream_t stream)
 {
     CUtensorMap qmap, kmap, vmap;
     if (!encode_pages(&kmap, kv.k, kv) || !encode_pages(&vmap, kv.v, kv) ||
@@ -767,6 +782,8 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.pv = pv;
     a.score = score_args(q.softmax_scale, q.softcap);
     a.table = kv.table;
+    a.table_stride = kv.table_stride;
+    a.max_len = max_len;
     a.n_heads = kv.n_kv_heads * q.group;
     a.n_pages = kv.n_pages;
     a.page_shift = kv.page_shift;

@@ -481,7 +481,7 @@ fathom_status fathom_qk_norm_rope(int32_t n_tokens, int32_t head_dim, const int3
  * A page table is device int32 [n_seqs][table_stride]: key j of sequence b
  * lies in slot j % page_size of page page_table[b][j / page_size].
  * Sequences may share pages.  Entries behind a sequence's last key are never
- * read.  A page index outside [0, n_pages) is never dereferenced and sets
+ * used.  A page index outside [0, n_pages) is never dereferenced and sets
  * FATHOM_ERR_INVALID_ARG in the device status (what it was to hold is
  * skipped). */
 typedef struct {
@@ -529,8 +529,9 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  *   out[b][i] = sum_j softmax(s)_j V_j,  j in [0, n).
  * A sequence of length 0 (a padded batch row) gets zeros.
  * prefix_len > 0 states that the first prefix_len keys (a multiple of
- * page_size) are the same pages in every row of the table: they are read from
- * the first row and multiplied with the queries of all sequences at once.
+ * page_size) are the same pages in the table's row of every sequence that has
+ * keys: they are looked up in one such row and multiplied with the queries of
+ * all sequences at once.  The row of an empty sequence may hold anything.
  * Every length is then 0 or at least prefix_len.  seq_lens (device int32
  * [n_seqs]) may change between replays of a captured call; max_len is the
  * host's bound on them.  A length that is negative, above max_len or, if not
