@@ -47,7 +47,7 @@ EXPORTED = (
     "fathom_n_words", "fathom_status_str", "fathom_pack_workspace_bytes", "fathom_pack_keys",
     "fathom_plan", "fathom_fixed_plan", "fathom_scan_workspace_bytes", "fathom_scan_topk",
     "fathom_scan_batched_workspace_bytes", "fathom_scan_topk_batched",
-    "fathom_last_device_status", "fathom_launch_count", "fathom_profile_read",
+    "fathom_last_device_status", "fathom_launch_count", "fathom_set_wait_limit", "fathom_profile_read",
     "fathom_scan_topk_static", "fathom_link_probe", "fathom_append_keys",
     "fathom_sparse_attention_workspace_bytes", "fathom_sparse_attention", "fathom_plan_marginal",
     "fathom_merge_topk",
@@ -139,6 +139,7 @@ def load_library(path: str = LIB_PATH):
         "fathom_scan_topk_batched": ([IX, I32, P, P, P, I32, P, P, P, SZ, U32, P], ctypes.c_int),
         "fathom_last_device_status": ([P], ctypes.c_int),
         "fathom_launch_count": ([], ctypes.c_uint64),
+        "fathom_set_wait_limit": ([ctypes.c_uint64], ctypes.c_uint64),
         "fathom_link_probe": ([P, SZ, P, P], ctypes.c_int),
         "fathom_profile_read": ([ctypes.POINTER(ctypes.c_double),
                                  ctypes.POINTER(ctypes.c_uint64)], ctypes.c_int),
@@ -432,6 +433,11 @@ def fathom_link_probe(buffer, nbytes: int, sink, stream=None):
 
 def fathom_launch_count() -> int:
     return int(load_library().fathom_launch_count())
+
+
+def fathom_set_wait_limit(ns: int) -> int:
+    """Limit of the waits inside kernels, in nanoseconds; returns the one before."""
+    return int(load_library().fathom_set_wait_limit(int(ns)))
 
 
 def fathom_profile_read():

@@ -19,6 +19,7 @@ __device__ int g_device_status;
 
 namespace {
 std::atomic<unsigned long long> g_launches{0};
+std::atomic<unsigned long long> g_wait_ns{500000000};
 std::mutex g_mu;
 int *g_status_ptr[64] = {nullptr};
 struct EventPair {
@@ -42,6 +43,8 @@ int *device_status_ptr()
 }
 
 void note_launch(int n) { g_launches.fetch_add((unsigned long long)n); }
+
+unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 
 cudaError_t note_error(cudaError_t e, const char *site)
 {
@@ -416,6 +419,8 @@ fathom_status fathom_last_device_status(cudaStream_t stream)
 }
 
 uint64_t fathom_launch_count(void) { return (uint64_t)g_launches.load(); }
+
+uint64_t fathom_set_wait_limit(uint64_t ns) { return (uint64_t)g_wait_ns.exchange(ns); }
 
 fathom_status fathom_profile_read(double *scan_kernel_ms, uint64_t *scan_kernel_launches)
 {

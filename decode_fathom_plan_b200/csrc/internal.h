@@ -24,6 +24,8 @@ struct NvtxRange {
 int *device_status_ptr();
 // Count one kernel launch (for fathom_launch_count).
 void note_launch(int n = 1);
+// Limit of a kernel's wait in nanoseconds (fathom_set_wait_limit).
+unsigned long long wait_limit_ns();
 // Record the CUDA error of a failed step (reported on stderr once per site
 // by the C-ABI layer) and return it.
 cudaError_t note_error(cudaError_t e, const char *site);

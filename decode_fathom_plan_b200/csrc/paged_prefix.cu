@@ -31,10 +31,12 @@
 // with V is issued after 7900 cycles: page table, copies, scores and softmax
 // in turn.
 //
-// Every wait has a time limit; where one runs out the CTA records
-// FATHOM_ERR_TIMEOUT, waits for its copies and products and leaves.  A barrier
-// is waited for by the parity of its phase, so whoever waits must have seen
-// the phase before: see the barriers of a step, and passing on.
+// Every wait has a time limit.  Where one runs out all warps stop at their next
+// one; when they are together again the CTA waits (with a limit) for every copy
+// and product that it issued, marks its parts as holding no key, so that
+// nothing that was not written is joined, and records FATHOM_ERR_TIMEOUT.  A
+// barrier is waited for by the parity of its phase, so whoever waits must have
+// seen the phase before: see the barriers of a step, and passing on.
 #include <cuda.h>
 #include <math.h>
 
@@ -51,8 +53,8 @@ constexpr int kRows = 128;                       // rows of a slot
 constexpr int kTile = 128;                       // keys of a tile
 constexpr int kStep = 64;                        // keys of a product
 constexpr int kBlockBytes = kTile * 128;         // 128 rows of 64 channels (128 bytes, swizzled)
-constexpr unsigned long long kWaitNs = 500000000ull;
-constexpr unsigned long long kSettleNs = 1000000ull;   // for copies under way after a stop
+constexpr unsigned long long kSettleNs = 500000000ull;  // for what is under way after a stop
+constexpr unsigned long long kTryNs = 100000ull;        // that one try of a wait may last
 constexpr int kTmemCols = 512;
 constexpr int kStageBytes = 4 * 32 * 128;        // 32 channels of a slot's rows in float32
 
@@ -72,6 +74,7 @@ struct PrefixArgs {
     PagedQuery q;
     PartsView pv;
     ScoreArgs score;
+    unsigned long long wait_ns;                  // limit of a wait
     const int32_t *table;
     int table_stride, max_len;
     int n_heads, n_pages, page_shift, head_dim;
@@ -97,15 +100,24 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+// Whether the phase of the given parity is over; waits up to ns for it, where that is 0 not at all.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t ns)
 {
     uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if (ns == 0)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(ns)
+            : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ unsigned long long global_ns()
@@ -117,17 +129,18 @@ __device__ __forceinline__ unsigned long long global_ns()
 // Waits for the phase of the given parity, the whole warp together; false once
 // *stop is set or the limit is over (which sets it).  Inlined: the warps that
 // issue products and copies make no calls.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *stop)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *stop, unsigned long long limit)
 {
-    bool ok = mbar_try(bar, parity);
+    const uint32_t once = (uint32_t)(limit < kTryNs ? limit : kTryNs);
+    bool ok = mbar_try(bar, parity, once);
     if (!ok) {
         const unsigned long long start = global_ns();
         do {
-            ok = mbar_try(bar, parity);
-            if (!ok && (*stop || global_ns() - start > kWaitNs)) {
+            if (*stop || global_ns() - start >= limit) {
                 *stop = 1;
                 break;
             }
+            ok = mbar_try(bar, parity, once);
         } while (!ok);
     }
     return __all_sync(0xFFFFFFFFu, ok);
@@ -136,7 +149,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void wait_anyway(uint32_t bar, uint32_t parity)
 {
     const unsigned long long start = global_ns();
-    while (!mbar_try(bar, parity) && global_ns() - start < kWaitNs) {
+    while (!mbar_try(bar, parity, (uint32_t)kTryNs) && global_ns() - start < kSettleNs) {
     }
     __syncwarp();
 }
@@ -294,6 +307,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     __shared__ alignas(8) uint64_t s_bar[kBarriers];
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
+    // parity of the last phase of each stage that a copy was issued for, -1 for none
+    __shared__ int s_copied[kStages];
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
     const uint32_t q_addr = base, ring = base + Shape::kQueryBytes, bars = smem_u32(s_bar);
     const auto bar = [&](int i) { return bars + 8 * i; };
@@ -307,6 +322,15 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     const int d = a.head_dim, G = a.q.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *stop = &s_stop;
+    // sequence of row r of slot s, and the place of its part; -1 where there is none
+    const auto sequence_of = [&](int s, int r) {
+        const int seq = seq0 + (shared ? s * a.slot_seqs : 0) + r / G;
+        return r < a.slot_seqs * G && seq < a.seqs ? seq : -1;
+    };
+    const auto place_of = [&](int s, int r) {
+        const int seq = sequence_of(s, r), part = shared ? split : split * kSlots + s;
+        return seq < 0 ? -1ll : ((long long)seq * a.n_heads + h * G + r % G) * a.parts + part;
+    };
     const uint32_t o_col = kSlots * kTile;                      // O of slot s at o_col + s*d
 
     if (warp == 0) {
@@ -314,6 +338,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         for (int i = lane; i < kBarriers; i += 32)
             mbar_init(bar(i), i >= kEmpty && i < kScores ? kSlots : i >= kProbs && i < kDone ? 4 : 1);
         if (lane == 0) s_stop = 0;
+        if (lane < kStages) s_copied[lane] = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 || warp == 3) {
@@ -364,10 +389,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
         }
         Place<kStages> at;
-        int issued = 0;
         bool ok = true, bad = false;
         const auto load = [&](bool mine, int tile) {
-            if (ok && mine) ok = mbar_wait(bar(kEmpty + at.stage), at.phase ^ 1, stop);
+            if (ok && mine) ok = mbar_wait(bar(kEmpty + at.stage), at.phase ^ 1, stop, a.wait_ns);
             if (ok && mine) {
                 int p = page;
                 if (lane >= boxes || (t0 + tile) * kTile + lane * box >= keys_end) {
@@ -379,7 +403,10 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 page = page_of(tile + 1);
                 const uint32_t dst = ring + at.stage * kTileBytes, full = bar(kFull + at.stage);
                 const int slot0 = ((t0 + tile) * kTile) & ((1 << shift) - 1);   // a page may hold several tiles
-                if (elect_one()) mbar_expect(full, kTileBytes);
+                if (elect_one()) {
+                    s_copied[at.stage] = (int)at.phase;
+                    mbar_expect(full, kTileBytes);
+                }
                 __syncwarp();
 #pragma unroll 1
                 for (int x = 0; x < boxes; ++x) {
@@ -390,7 +417,6 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                             tma_load(dst + cb * kBlockBytes + x * box * 128, map, full, cb * 64, slot0, h, px);
                 }
                 __syncwarp();
-                ++issued;
             }
             at.next();
         };
@@ -403,13 +429,6 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 if (j + 2 < walk.steps(s)) load(keys, walk.tile((j + 2) >> 1, s));
             }
         if (bad) set_status(a.status, FATHOM_ERR_INVALID_ARG);
-        if (!ok && issued) {                                    // let the copies land
-            if (keys) wait_anyway(bar(kQueries), 0);
-            const unsigned long long start = global_ns();
-            while (global_ns() - start < kSettleNs) {
-            }
-            __syncwarp();
-        }
     } else if (warp < 4) {
         // ---------------------------------------------------- products: a warp for each slot, so
         // that one waits and prepares while the other's are in the pipe
@@ -436,16 +455,16 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             const int takers = walk.takers(), steps = walk.steps(me);
             Place<kStages> at;
             int k = 0, v = 0;                                   // stages of the tiles in use
-            bool ok = mbar_wait(bar(kQueries), 0, stop);
+            bool ok = mbar_wait(bar(kQueries), 0, stop, a.wait_ns);
             const auto take = [&](int &stage) {
                 stage = at.stage;
-                ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop);
+                ok = ok && mbar_wait(bar(kFull + at.stage), at.phase, stop, a.wait_ns);
                 at.next();
             };
             // The other slot's tile is passed on: seen full and freed.  A warp that left such phases
             // out could come back to a stage two of them early, which their parity does not show.
             const auto pass = [&](const Place<kStages> &of) {
-                ok = ok && mbar_wait(bar(kFull + of.stage), of.phase, stop);
+                ok = ok && mbar_wait(bar(kFull + of.stage), of.phase, stop, a.wait_ns);
                 if (ok && elect_one()) mbar_arrive(bar(kEmpty + of.stage));
                 __syncwarp();
             };
@@ -497,7 +516,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     }
                 if (j < steps) {
                     const uint64_t v_desc = v_ring + v * kStageStep + (j & 1) * kHalfStep;
-                    ok = ok && mbar_wait(bar(kProbs + 2 * me + (j & 1)), (j >> 1) & 1, stop);
+                    ok = ok && mbar_wait(bar(kProbs + 2 * me + (j & 1)), (j >> 1) & 1, stop, a.wait_ns);
                     tc_after();
                     if (ok && elect_one()) {
                         // O += P V of step j; then S of step j + 2 goes where P was
@@ -518,17 +537,12 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 if (n_others > 0) pass(others[0]);
                 if (n_others > 1) pass(others[1]);
             }
-            if (!ok) {                                          // let the products end
-                if (elect_one()) umma_commit(bar(kDrained + me));
-                __syncwarp();
-                wait_anyway(bar(kDrained + me), 0);
-            }
         }
     } else {
         // ----------------------------------------------------- softmax
         const int s = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-        const int seq = seq0 + (shared ? s * a.slot_seqs : 0) + r / G;
-        const bool mine = r < a.slot_seqs * G && seq < a.seqs;
+        const int seq = sequence_of(s, r);
+        const bool mine = seq >= 0;
         const bool live = __any_sync(0xFFFFFFFFu, mine);
         const int b = mine ? seq : 0, head = h * G + r % G;
         const int seq_len = a.q.seq_lens[b];
@@ -544,7 +558,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         for (int j = 0; j < steps; ++j) {
             const int which = 2 * s + (j & 1);
             const uint32_t s_addr = lane_addr + s * kTile + (j & 1) * kStep;
-            ok = mbar_wait(bar(kScores + which), (j >> 1) & 1, stop);
+            ok = mbar_wait(bar(kScores + which), (j >> 1) & 1, stop, a.wait_ns);
             if (!ok) break;
             tc_after();
             if (live) {
@@ -574,7 +588,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                     m = next;
                     l *= w;
                     if (j > 0) {
-                        ok = mbar_wait(bar(kDone + 2 * s + ((j - 1) & 1)), ((j - 1) >> 1) & 1, stop);
+                        ok = mbar_wait(bar(kDone + 2 * s + ((j - 1) & 1)), ((j - 1) >> 1) & 1, stop,
+                                       a.wait_ns);
                         if (!ok) break;
                         tc_after();
 #pragma unroll 1
@@ -617,11 +632,10 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             if (elect_one()) mbar_arrive(bar(kProbs + which));
         }
         for (int x = 0; x < 2; ++x)
-            if (ok && steps > 0) ok = mbar_wait(bar(kDone + 2 * s + x), (steps / 2 - 1) & 1, stop);
+            if (ok && steps > 0) ok = mbar_wait(bar(kDone + 2 * s + x), (steps / 2 - 1) & 1, stop, a.wait_ns);
         if (ok && live) {
             tc_after();
-            const int part = shared ? split : split * kSlots + s;
-            const long long place = mine ? (long long)(b * a.n_heads + head) * a.parts + part : -1;
+            const long long place = place_of(s, r);
             if (mine) a.pv.ml[place] = make_float2(m, l);
             if (steps > 0) {
                 // 32 channels of the warp's 32 rows at a time through shared memory, so that a store
@@ -660,7 +674,22 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     }
     tc_before();
     __syncthreads();
-    if (threadIdx.x == 0 && s_stop) set_status(a.status, FATHOM_ERR_TIMEOUT);
+    if (*stop) {                                                // the same for all: no warp waits any more
+        if (warp == 0) {
+            wait_anyway(bar(kQueries), 0);
+            for (int x = 0; x < kStages; ++x)
+                if (s_copied[x] >= 0) wait_anyway(bar(kFull + x), s_copied[x]);
+            if (lane == 0) set_status(a.status, FATHOM_ERR_TIMEOUT);
+        } else if (warp <= kSlots) {
+            if (elect_one()) umma_commit(bar(kDrained + warp - 1));   // by the lane that issued the products
+            __syncwarp();
+            wait_anyway(bar(kDrained + warp - 1), 0);
+        } else if (warp >= 4) {
+            const long long place = place_of((warp - 4) >> 2, (warp & 3) * 32 + lane);
+            if (place >= 0) a.pv.ml[place] = make_float2(-INFINITY, 0.0f);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         __syncwarp();
         tc_after();
@@ -795,6 +824,7 @@ cudaError_t launch_paged_prefix(const PagedView &kv, const PagedQuery &q, const 
     a.split_rest = p.n_tiles % p.splits;
     a.two_blocks = p.two_blocks;
     a.parts = p.parts;
+    a.wait_ns = wait_limit_ns();
     a.status = device_status_ptr();
     const dim3 ctas(p.row_groups, kv.n_kv_heads, p.splits);
     return kv.dtype == FATHOM_BF16 ? launch_type<__nv_bfloat16>(qmap, kmap, vmap, a, ctas, stream)

@@ -586,6 +586,16 @@ fathom_status fathom_last_device_status(cudaStream_t stream);
 /* Kernels this library has launched in this process. */
 uint64_t fathom_launch_count(void);
 
+/* Set the limit in nanoseconds of every wait inside a kernel, for the calls
+ * from now on in this process (a captured call keeps the one it was captured
+ * with); returns the limit before, at first 500 ms.  Waits are short, so one
+ * that runs out means a GPU that was taken away for that long, or a fault:
+ * the call ends, sets FATHOM_ERR_TIMEOUT in the device status, and its outputs
+ * are not to be used.  Only fathom_paged_attention's kernel of a shared prefix
+ * waits; its rows then lack keys of the prefix.  0: a wait that is not over at
+ * its first look is given up (for tests). */
+uint64_t fathom_set_wait_limit(uint64_t ns);
+
 /* Time of what FATHOM_SCAN_PROFILE times (the fetch sequence for a
  * host-resident index, else the main scan kernel), recorded with CUDA events:
  * synchronises on the recorded events and returns the summed milliseconds

@@ -64,3 +64,50 @@ def test_prefix_of_a_batch_of_padded_rows_alone():
     b.attention()
     assert status() == fp.FATHOM_OK                 # no entry of the table was used
     assert (b.out == 0).all()
+
+
+# ---------------------------------------------------------------------- waits that run out
+@pytest.fixture
+def limit():
+    before = fp.fathom_set_wait_limit(500000000)
+    assert before == 500000000
+    yield fp.fathom_set_wait_limit
+    fp.fathom_set_wait_limit(before)
+
+
+WAITS = [
+    # lens, H, G, d, dtype: two row blocks, the even and odd tiles of one, one slot
+    ([2048 + 37 * (i % 4) for i in range(40)], 2, 4, 128, BF16),
+    ([4096 + 5 * i for i in range(5)], 4, 3, 64, F16),
+    ([2048, 0, 2100, 2300], 4, 8, 256, BF16),
+]
+
+
+@pytest.mark.parametrize("lens,H,G,d,dtype", WAITS)
+def test_a_wait_that_runs_out_is_reported_and_joins_nothing_unwritten(lens, H, G, d, dtype, limit):
+    prefix = lens[0]
+    b = shared(lens, dtype, prefix, H, G, d)
+    b.attention()
+    assert status() == fp.FATHOM_OK
+    whole = b.out.clone()
+    # no wait is over at its first look: what is left are the keys behind the prefix
+    limit(0)
+    b.ws.fill_(0xFF)                                # parts that nobody writes are NaN
+    b.attention(ws=b.ws)
+    assert status() == fp.FATHOM_ERR_TIMEOUT and status() == fp.FATHOM_OK
+    own = np.full((len(lens), H * G, max(lens) - prefix), -1)
+    for s, n in enumerate(lens):
+        own[s, :, :max(0, n - prefix)] = np.arange(prefix, max(n, prefix))
+    want, tol = b.expect(idx=own)
+    check(b.out, want, tol)
+    # limits that run out with copies and products under way
+    for ns in (200, 1000, 3000, 6000, 12000, 25000):
+        limit(ns)
+        for _ in range(3):
+            b.ws.fill_(0xFF)
+            b.attention(ws=b.ws)
+            assert status() in (fp.FATHOM_OK, fp.FATHOM_ERR_TIMEOUT)
+            assert torch.isfinite(b.out).all()
+    limit(500000000)
+    b.attention(ws=b.ws)
+    assert status() == fp.FATHOM_OK and torch.equal(b.out, whole)
