@@ -254,7 +254,7 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
     if (!cache_ok(cache) || n_seqs < 1 || n_seqs > kMaxSequences || group < 1 || group > kMaxGroup ||
         max_len < 1 || prefix_len < 0 || prefix_len > max_len || prefix_len % cache->page_size)
         return 0;
-    return paged_attention_bytes(cache->n_kv_heads, cache->head_dim, n_seqs, group, max_len, prefix_len);
+    return paged_attention_most_bytes(cache->n_kv_heads, cache->head_dim, n_seqs, group, max_len, prefix_len);
 }
 
 fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_rows *q,
@@ -289,7 +289,7 @@ size_t fathom_sparse_attention_paged_workspace_bytes(int32_t n_seqs, int32_t n_h
     if (n_seqs < 1 || n_seqs > kMaxSequences || n_heads < 1 || n_heads > kMaxHeads || k < 1 ||
         k > kMaxList || !head_dim_ok(head_dim) || (long long)n_seqs * n_heads >= (1ll << 31))
         return 0;
-    return paged_sparse_bytes(n_seqs * n_heads, head_dim, k);
+    return paged_sparse_most_bytes(n_seqs * n_heads, head_dim, k);
 }
 
 fathom_status fathom_sparse_attention_paged(const fathom_kv_cache *cache, const fathom_rows *q,

@@ -177,11 +177,15 @@ struct PagedQuery {              // the query rows, the scores and the output ro
     float softmax_scale, softcap;
     int n_seqs, group;
 };
+// What a call uses, and the most that any call of up to these sizes does.
 size_t paged_attention_bytes(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len,
                              int prefix_len);
+size_t paged_attention_most_bytes(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len,
+                                  int prefix_len);
 cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int max_len,
                                    int prefix_len, void *ws, cudaStream_t stream);
 size_t paged_sparse_bytes(int n_rows, int head_dim, int k);
+size_t paged_sparse_most_bytes(int n_rows, int head_dim, int k);
 cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const int32_t *idx, int k,
                                 void *ws, cudaStream_t stream);
 

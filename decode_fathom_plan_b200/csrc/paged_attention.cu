@@ -498,6 +498,26 @@ size_t paged_attention_bytes(int n_kv_heads, int head_dim, int n_seqs, int group
     return parts_bytes(p.places, head_dim) + round16((size_t)n_seqs * n_kv_heads * sizeof(int2));
 }
 
+// A smaller batch may have more parts: fewer blocks of rows are split into more runs.  Between two
+// multiples of the sequences of a slot the runs are the same, so the most rows have the most places;
+// from 148 blocks on there is one run.  Runs grow with the prefix and CTAs with the own keys, which
+// are all of them where the prefix is left out.
+size_t paged_attention_most_bytes(int n_kv_heads, int head_dim, int n_seqs, int group, int max_len,
+                                  int prefix_len)
+{
+    size_t most = 0;
+    const auto consider = [&](long long seqs) {
+        const size_t parts = plan_prefix(n_kv_heads, head_dim, (int)seqs, group, prefix_len).parts;
+        if (parts) most = std::max(most, (size_t)seqs * n_kv_heads * group * (parts + 1));
+    };
+    const int slot = plan_prefix(n_kv_heads, head_dim, n_seqs, group, prefix_len).slot_seqs;
+    consider(n_seqs);
+    if (slot)
+        for (int i = 1; i <= 2 * 149 && (long long)i * slot < n_seqs; ++i) consider((long long)i * slot);
+    const size_t places = most + (size_t)split_ctas(n_kv_heads, head_dim, n_seqs, max_len) * 2 * group;
+    return parts_bytes(places, head_dim) + round16((size_t)n_seqs * n_kv_heads * sizeof(int2));
+}
+
 cudaError_t launch_paged_attention(const PagedView &kv, const PagedQuery &q, int max_len,
                                    int prefix_len, void *ws, cudaStream_t stream)
 {

@@ -216,10 +216,12 @@ cudaError_t launch_sparse(const SparseArgs &a, dim3 grid, cudaStream_t stream)
 
 // Keys of a CTA: a group of 32 for each warp, or several (whose look-ups then overlap) where
 // there are rows enough.
+constexpr int kLeastRun = 128, kMostRun = 512;
+constexpr long long kFullGpu = 148 * 8;
 int sparse_run_keys(int n_rows, int k)
 {
-    const long long groups = (long long)n_rows * k / (148 * 8);
-    return (int)std::min<long long>(std::max<long long>(groups / 128 * 128, 128), 512);
+    const long long groups = (long long)n_rows * k / kFullGpu;
+    return (int)std::min<long long>(std::max<long long>(groups / kLeastRun * kLeastRun, kLeastRun), kMostRun);
 }
 int sparse_runs(int n_rows, int k) { return (k - 1) / sparse_run_keys(n_rows, k) + 1; }
 
@@ -229,6 +231,24 @@ size_t paged_sparse_bytes(int n_rows, int head_dim, int k)
 {
     const int runs = sparse_runs(n_rows, k);
     return runs == 1 ? 0 : parts_bytes((size_t)n_rows * runs, head_dim);
+}
+
+// Fewer rows or keys may have more runs.  Runs of r keys (but the longest) are taken while
+// rows * k < kFullGpu * (r + kLeastRun) = p, and rows have several only where k > r: then there are
+// at most p / r rows, with rows * ceil(k / r) <= p / r + rows parts.
+size_t paged_sparse_most_bytes(int n_rows, int head_dim, int k)
+{
+    long long most = 0;
+    for (int r = kLeastRun; r <= kMostRun; r += kLeastRun) {
+        if (k <= r) break;
+        long long parts = (long long)n_rows * ((k - 1) / r + 1);
+        if (r < kMostRun) {
+            const long long p = kFullGpu * (r + kLeastRun);
+            parts = std::min(parts, p / r + std::min<long long>(n_rows, p / r));
+        }
+        most = std::max(most, parts);
+    }
+    return most ? parts_bytes((size_t)most, head_dim) : 16;
 }
 
 cudaError_t launch_paged_sparse(const PagedView &kv, const PagedQuery &q, const int32_t *idx, int k,

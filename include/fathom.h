@@ -515,7 +515,11 @@ fathom_status fathom_append_kv(const fathom_kv_cache *cache, int32_t n_tokens, c
                                const fathom_rotary *rotary, const void *k_weight, float eps,
                                cudaStream_t stream);
 
-/* Workspace bytes fathom_paged_attention needs (0 for invalid sizes). */
+/* Workspace bytes for fathom_paged_attention, 0 only for invalid sizes: enough
+ * for every call with the cache's heads and head_dim, this group, and up to this
+ * many sequences, this max_len and this prefix_len, so that a workspace of the
+ * largest batch serves as sequences come and go.  (A call uses no more than it
+ * needs, which may be less for the larger of two batches.) */
 size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int32_t n_seqs,
                                               int32_t group, int32_t max_len, int32_t prefix_len);
 
@@ -551,7 +555,9 @@ fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_
                                      const float *slopes, const fathom_rows *out, void *workspace,
                                      size_t workspace_bytes, cudaStream_t stream);
 
-/* Workspace bytes fathom_sparse_attention_paged needs (0 for invalid sizes). */
+/* Workspace bytes for fathom_sparse_attention_paged, 0 only for invalid sizes:
+ * enough for every call with this head_dim and up to this many sequences, heads
+ * and listed keys.  (A call that needs none takes NULL.) */
 size_t fathom_sparse_attention_paged_workspace_bytes(int32_t n_seqs, int32_t n_heads,
                                                      int32_t head_dim, int32_t k);
 

@@ -111,3 +111,30 @@ def test_a_wait_that_runs_out_is_reported_and_joins_nothing_unwritten(lens, H, G
     limit(500000000)
     b.attention(ws=b.ws)
     assert status() == fp.FATHOM_OK and torch.equal(b.out, whole)
+
+
+# ------------------------------------------------ one workspace while sessions come and go
+def test_one_workspace_for_the_largest_batch_and_every_smaller_one():
+    G, d, prefix = 4, 128, 2048
+    b = shared([prefix + 9 * i for i in range(40)], BF16, prefix, 8, G, d)
+    longest = max(b.lens)
+    need = fp.fathom_paged_attention_workspace_bytes(b.kv.desc, 40, G, longest, prefix)
+    hq, k = 8 * G, 600
+    idx = torch.arange(k, dtype=torch.int32, device="cuda").repeat(40, hq, 1)
+    need_sparse = fp.fathom_sparse_attention_paged_workspace_bytes(40, hq, d, k)
+    guard, guard_sparse = (torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+                           for n in (need, need_sparse))
+    q, out, table, lens_t, lens = b.q, b.out, b.table_t, b.lens_t, b.lens
+    for n in (40, 33, 32, 21, 2, 1):
+        b.lens, b.lens_t, b.table_t = lens[:n], lens_t[:n], table[:n]
+        b.q, b.out = q[:n], out[:n]
+        b.attention(max_len=longest, ws=guard[:need])
+        check_rows(b, {(0, 0), (n - 1, hq - 1), (n // 2, 5)})
+        fp.fathom_sparse_attention_paged(b.kv.desc, b.q, idx[:n], b.table_t, b.lens_t, b.out,
+                                         guard_sparse[:need_sparse], b.scale)
+        at = {(0, 0), (n - 1, hq - 1), (n // 2, 5)}
+        want, tol = b.expect(idx=idx[:n].cpu().numpy(), rows=at, round_p=False)
+        rows = tuple(np.array(sorted(at)).T)
+        check(b.out.cpu()[rows], want[rows], tol[rows])
+    assert status() == fp.FATHOM_OK
+    assert (guard[need:] == 0xA5).all() and (guard_sparse[need_sparse:] == 0xA5).all()
