@@ -187,4 +187,18 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 // accuracy, fits float16, and most tiles then rescale nothing.
 constexpr float kRescale = 8.0f;
 
+// The reference that probabilities of type T are relative to for their product
+// with V, from the reference maximum m.  A float16 is a multiple of 2^-24, so
+// far below 1 a probability has few bits and then none; relative to 2^7 below m
+// it is at most 2^15, which float16 holds, and its half step at most 2^-32 of
+// the largest weight.  (Relative to m itself, keys 17.2 and 17.4 nats below
+// another had 1.4 times and half their weight.)  A bfloat16 has the range of a
+// float.  Parts keep this reference beside their sums.
+template <typename T>
+__device__ __forceinline__ float prob_reference(float m);
+template <>
+__device__ __forceinline__ float prob_reference<__nv_bfloat16>(float m) { return m; }
+template <>
+__device__ __forceinline__ float prob_reference<__half>(float m) { return m - 7.0f; }
+
 }  // namespace fathom

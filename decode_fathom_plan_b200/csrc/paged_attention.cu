@@ -30,7 +30,8 @@
 // P is rounded to the cache's type for its product.  For bfloat16 it is split
 // into two terms (its rounding and what that left): 8 bits of P would add as
 // much error again as the rounding of the output itself, and the second
-// product is free under the loads.
+// product is free under the loads.  A float16 P is relative to a reference 2^7
+// lower, so that small probabilities keep their bits.
 //
 // The keys of all sequences and KV heads are one list of blocks of 64, dealt
 // out evenly: CTA i of N takes blocks [i*total/N, (i+1)*total/N), so one wave of
@@ -355,7 +356,7 @@ paged_split_kernel(const SplitArgs a)
                 float p[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float ref = m[x & 1] == -INFINITY ? 0.0f : m[x & 1];
+                    const float ref = m[x & 1] == -INFINITY ? 0.0f : prob_reference<T>(m[x & 1]);
                     p[x] = exp2_fast(c[u][x] - ref);
                     if (kSplitP) l[x & 1] += p[x];
                 }
@@ -391,7 +392,7 @@ paged_split_kernel(const SplitArgs a)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], off);
             if (g == 0) {
-                s_m[warp][2 * t + x] = m[x];
+                s_m[warp][2 * t + x] = prob_reference<T>(m[x]);
                 s_l[warp][2 * t + x] = l[x];
             }
 #pragma unroll

@@ -603,7 +603,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                         }
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : m;
+                const float ref = m == -INFINITY ? 0.0f : prob_reference<T>(m);
                 const Pair mult2(mult, mult), ref2(-ref, -ref);
                 Pair sum[4];
 #pragma unroll
@@ -636,7 +636,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         if (ok && live) {
             tc_after();
             const long long place = place_of(s, r);
-            if (mine) a.pv.ml[place] = make_float2(m, l);
+            if (mine) a.pv.ml[place] = make_float2(prob_reference<T>(m), l);
             if (steps > 0) {
                 // 32 channels of the warp's 32 rows at a time through shared memory, so that a store
                 // is four rows of 128 bytes (a lane's own row at a time: 32 rows, 1.6 us longer)

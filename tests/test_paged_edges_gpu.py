@@ -138,3 +138,34 @@ def test_one_workspace_for_the_largest_batch_and_every_smaller_one():
         check(b.out.cpu()[rows], want[rows], tol[rows])
     assert status() == fp.FATHOM_OK
     assert (guard[need:] == 0xA5).all() and (guard_sparse[need_sparse:] == 0xA5).all()
+
+
+# ------------------------------------------------- one key that outweighs a long tail of others
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,prefix,H", [([1024] * 8, 0, 32), ([516, 515], 512, 75)])
+@pytest.mark.parametrize("nats", [8.0, 13.0, 16.0, 17.2, 17.4])
+def test_a_key_far_above_the_others_leaves_them_their_weight(lens, prefix, H, dtype, nats):
+    """A key whose value is zero takes nearly all of the weight; what is left are the others.
+
+    A float16 probability is a multiple of 2^-24 at least, half a step 2^-25, of a scale 2^7 times
+    that of the reference maximum, which is at most the row's maximum: 2^-32 of the largest weight.
+    At 17.2 nats a key weighs 2^-24.8 of it, so its rounding is 2^-7.2 of it, and that of all of
+    them 1 in 140 of the result, whatever their number."""
+    d = 64
+    b = Batch(lens, prefix, H, 1, d, 16, dtype, False, 5)
+    assert not prefix or 4 * d * H * prefix * (len(lens) - 1) >= 8 << 20
+    k, v = torch.zeros_like(b.kv.k), (64 * (1 + b.kv.v * 0.1)).to(dtype)
+    for s in range(len(lens)):
+        k[b.table[s, 0], :, 0, 0], v[b.table[s, 0], :, 0] = nats, 0.0
+    b.kv.k.copy_(k)
+    b.kv.v.copy_(v)
+    b.k64, b.v64 = po.f64(b.kv.k), po.f64(b.kv.v)
+    b.q.zero_()
+    b.q[:, :, 0] = 8.0                                      # times 1/sqrt(64): a score is the key's first channel
+    b.attention()
+    assert status() == fp.FATHOM_OK
+    q, step, tiny = po.f64(b.q), po.HALF_STEP[dtype], po.TINY[dtype]
+    for s, i in ((0, 0), (len(lens) - 1, H - 1), (1, H // 2)):
+        ks, vs = (po.gather(p, b.table[s], np.arange(lens[s]), i, 16) for p in (b.k64, b.v64))
+        want, err = po.attend(q[s, i], ks, vs, np.zeros(lens[s]), b.scale, p_step=step, p_tiny=tiny * 2.0 ** -7)
+        check(b.out[s, i], want, err + step * np.abs(want) * 1.01 + tiny, (s, i))
