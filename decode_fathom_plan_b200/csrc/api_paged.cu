@@ -13,6 +13,13 @@ namespace {
 constexpr int kMaxHeads = 65535;      // also the y and z extent of a grid
 constexpr int kMaxSequences = 65535;
 constexpr int kMaxList = 1 << 28;     // listed keys of a query
+// Keys of a sequence: numbers of keys are int, and run up to a block past the last one; so is the
+// number of a block of 64 among those of all KV heads.
+constexpr int kMaxLength = INT32_MAX - 65535;
+bool length_ok(int max_len, int n_kv_heads)
+{
+    return max_len >= 1 && max_len <= kMaxLength && (max_len / 64 + 1ll) * n_kv_heads <= INT32_MAX;
+}
 
 fathom_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FATHOM_OK : FATHOM_ERR_CUDA; }
 
@@ -252,7 +259,7 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
                                               int32_t group, int32_t max_len, int32_t prefix_len)
 {
     if (!cache_ok(cache) || n_seqs < 1 || n_seqs > kMaxSequences || group < 1 || group > kMaxGroup ||
-        max_len < 1 || prefix_len < 0 || prefix_len > max_len || prefix_len % cache->page_size)
+        !length_ok(max_len, cache->n_kv_heads) || prefix_len < 0 || prefix_len > max_len || prefix_len % cache->page_size)
         return 0;
     return paged_attention_most_bytes(cache->n_kv_heads, cache->head_dim, n_seqs, group, max_len, prefix_len);
 }
@@ -267,7 +274,7 @@ fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_
     NvtxRange range("fathom_paged_attention");
     if (!cache_ok(cache) || !page_table || !seq_lens) return FATHOM_ERR_INVALID_ARG;
     const int group = query_group(cache, q, out, n_seqs, softmax_scale, softcap);
-    if (!group || max_len < 1 || prefix_len < 0 || prefix_len > max_len ||
+    if (!group || !length_ok(max_len, cache->n_kv_heads) || prefix_len < 0 || prefix_len > max_len ||
         prefix_len % cache->page_size || table_stride < 1 ||
         (long long)table_stride * cache->page_size < max_len)
         return FATHOM_ERR_INVALID_ARG;

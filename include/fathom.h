@@ -538,10 +538,11 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  * all sequences at once.  The row of an empty sequence may hold anything.
  * Every length is then 0 or at least prefix_len.  seq_lens (device int32
  * [n_seqs]) may change between replays of a captured call; max_len is the
- * host's bound on them.  A length that is negative, above max_len or, if not
- * 0, below prefix_len sets FATHOM_ERR_INVALID_ARG in the device status, and
- * that sequence gets zeros.  A key on a bad page is skipped (one of a shared
- * prefix may take part with a K and V of zeros instead).
+ * host's bound on them, at most 2^31 - 65536, and with max_len * n_kv_heads
+ * below 2^37 - 64 * n_kv_heads.  A length that is negative, above max_len or,
+ * if not 0, below prefix_len sets FATHOM_ERR_INVALID_ARG in the device status,
+ * and that sequence gets zeros.  A key on a bad page is skipped (one of a
+ * shared prefix may take part with a K and V of zeros instead).
  * q, out: rows of n_seqs tokens with G*n_kv_heads heads, in the cache's type,
  * 16-byte aligned, strides positive multiples of 8, n_seqs at most 65535; G
  * 1..8.  slopes: device float32

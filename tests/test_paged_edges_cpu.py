@@ -95,3 +95,25 @@ def test_a_valid_size_is_never_zero(lib):
         assert fp.fathom_sparse_attention_paged_workspace_bytes(1, 1, 32, k) > 0
     assert fp.fathom_sparse_attention_paged_workspace_bytes(1, 1, 32, 0) == 0
     assert fp.fathom_paged_attention_workspace_bytes(cache(1, 32), 1, 1, 1) > 0
+
+
+# -------------------------------------------------------------- lengths near the end of 32 bits
+def test_bounds_of_the_lengths_that_a_key_number_cannot_pass_are_refused(lib):
+    """Key numbers are int32 and run up to a block past the last key."""
+    c, q, most = cache(1, 32), rows(1, 32), 2 ** 31 - 2 ** 16
+
+    def call(max_len, prefix=0):
+        return lib.fathom_paged_attention(ctypes.byref(c), ctypes.byref(q), FAKE, 1 << 27, FAKE, 1, max_len, prefix,
+                                          0.1, 0.0, 0, ctypes.byref(q), 0, 0, 0)
+
+    size = fp.fathom_paged_attention_workspace_bytes
+    for heads, longest in ((65535, 2 ** 21 - 64), (128, 2 ** 30 - 128)):      # blocks of 64 of all KV heads
+        many, h = cache(heads, 32), rows(heads, 32)
+        for n, rc in ((longest, fp.FATHOM_ERR_WORKSPACE), (longest + 2 ** 12, fp.FATHOM_ERR_INVALID_ARG)):
+            assert lib.fathom_paged_attention(ctypes.byref(many), ctypes.byref(h), FAKE, 1 << 27, FAKE, 1, n, 0, 0.1,
+                                              0.0, 0, ctypes.byref(h), 0, 0, 0) == rc
+            assert (size(many, 1, 1, n) > 0) == (rc == fp.FATHOM_ERR_WORKSPACE)
+    assert call(most) == call(most, most) == fp.FATHOM_ERR_WORKSPACE and size(c, 1, 1, most, most) > 0
+    for longer in (most + 1, 2 ** 31 - 1):
+        assert call(longer) == call(longer, most) == fp.FATHOM_ERR_INVALID_ARG
+        assert size(c, 1, 1, longer) == size(c, 1, 1, longer, 16) == 0
