@@ -42,6 +42,7 @@ FATHOM_ROTARY_PLAIN = 0
 FATHOM_ROTARY_LINEAR = 1
 FATHOM_ROTARY_NTK = 2
 FATHOM_ROTARY_YARN = 3
+FATHOM_ROTARY_YARN_INDEX = 4
 
 EXPORTED = (
     "fathom_n_words", "fathom_status_str", "fathom_pack_workspace_bytes", "fathom_pack_keys",
@@ -574,11 +575,15 @@ class RotaryTable:
 
     rotary_dim: channels of a head that are rotated (default: all of
     head_dim).  interleaved: pairs are (2i, 2i + 1) instead of (i, i +
-    rotary_dim/2).  scaling: "none", "linear", "ntk" or "yarn", stretched by
-    factor (fathom_rotary_turns gives the formulas)."""
+    rotary_dim/2).  scaling: "none", "linear", "ntk", "yarn" or "yarn_index",
+    stretched by factor (include/fathom.h gives the formulas).  "yarn" is the
+    paper's, whose ramp runs over the turns of a pair; "yarn_index", whose ramp
+    runs over the pairs' numbers, is what checkpoints with beta_fast, beta_slow
+    and an original length in their configuration are trained with."""
 
     _SCALINGS = {"none": FATHOM_ROTARY_PLAIN, "linear": FATHOM_ROTARY_LINEAR,
-                 "ntk": FATHOM_ROTARY_NTK, "yarn": FATHOM_ROTARY_YARN}
+                 "ntk": FATHOM_ROTARY_NTK, "yarn": FATHOM_ROTARY_YARN,
+                 "yarn_index": FATHOM_ROTARY_YARN_INDEX}
 
     def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, base: float = 10000.0,
                  interleaved: bool = False, scaling: str = "none", factor: float = 1.0,

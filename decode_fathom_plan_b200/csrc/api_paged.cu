@@ -152,26 +152,37 @@ fathom_status fathom_rotary_turns(double *turns, float *magnitude, int32_t rotar
 {
     if (!turns || !magnitude || rotary_dim < 2 || rotary_dim % 2 || !(base > 0.0) || !isfinite(base))
         return FATHOM_ERR_INVALID_ARG;
-    if (scaling < FATHOM_ROTARY_PLAIN || scaling > FATHOM_ROTARY_YARN) return FATHOM_ERR_INVALID_ARG;
+    if (scaling < FATHOM_ROTARY_PLAIN || scaling > FATHOM_ROTARY_YARN_INDEX) return FATHOM_ERR_INVALID_ARG;
     if (scaling != FATHOM_ROTARY_PLAIN && !(factor >= 1.0 && isfinite(factor)))
         return FATHOM_ERR_INVALID_ARG;
     if (scaling == FATHOM_ROTARY_NTK && rotary_dim < 4) return FATHOM_ERR_INVALID_ARG;
-    if (scaling == FATHOM_ROTARY_YARN &&
+    const bool by_index = scaling == FATHOM_ROTARY_YARN_INDEX, yarn = by_index || scaling == FATHOM_ROTARY_YARN;
+    if (by_index && !(base > 1.0 && beta_slow > 0.0)) return FATHOM_ERR_INVALID_ARG;
+    if (yarn &&
         (original_len < 1 || !(beta_fast > beta_slow) || !isfinite(beta_fast) || !isfinite(beta_slow)))
         return FATHOM_ERR_INVALID_ARG;
     const double pi2 = 6.283185307179586476925286766559;
     if (scaling == FATHOM_ROTARY_NTK) base *= pow(factor, rotary_dim / (rotary_dim - 2.0));
+    double low = 0.0, high = 0.0;             // pairs between which YARN_INDEX changes over
+    if (by_index) {
+        const auto pair = [&](double r) { return rotary_dim * log(original_len / (pi2 * r)) / (2.0 * log(base)); };
+        low = fmax(floor(pair(beta_fast)), 0.0);
+        high = fmin(ceil(pair(beta_slow)), rotary_dim - 1.0);
+        if (high < low) return FATHOM_ERR_INVALID_ARG;
+        if (low == high) high += 0.001;
+    }
     for (int i = 0; i < rotary_dim / 2; ++i) {
         double turn = pow(base, -2.0 * i / rotary_dim) / pi2;
         if (scaling == FATHOM_ROTARY_LINEAR) turn /= factor;
-        if (scaling == FATHOM_ROTARY_YARN) {
+        if (yarn) {
             const double r = (double)original_len * turn;
-            const double g = fmin(1.0, fmax(0.0, (r - beta_slow) / (beta_fast - beta_slow)));
+            const double at = by_index ? 1.0 - (i - low) / (high - low) : (r - beta_slow) / (beta_fast - beta_slow);
+            const double g = fmin(1.0, fmax(0.0, at));
             turn = turn * g + turn / factor * (1.0 - g);
         }
         turns[i] = turn;
     }
-    *magnitude = scaling == FATHOM_ROTARY_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    *magnitude = yarn ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
     return FATHOM_OK;
 }
 

@@ -432,7 +432,8 @@ typedef enum {
     FATHOM_ROTARY_PLAIN = 0,
     FATHOM_ROTARY_LINEAR = 1,
     FATHOM_ROTARY_NTK = 2,
-    FATHOM_ROTARY_YARN = 3
+    FATHOM_ROTARY_YARN = 3,
+    FATHOM_ROTARY_YARN_INDEX = 4
 } fathom_rotary_scaling;
 
 /* Host helper: fill the host array turns [rotary_dim/2] and *magnitude.
@@ -444,9 +445,20 @@ typedef enum {
  *           r = original_len * f_i / 2pi times over the original context has
  *           g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1)
  *           (Peng et al., "YaRN", 2023, the by-parts interpolation)
- * and magnitude 1, or 0.1*ln(factor) + 1 for YARN.
- * rotary_dim even and >= 2 (>= 4 for NTK), base > 0, factor >= 1 where it is
- * used, beta_fast > beta_slow and original_len >= 1 for YARN. */
+ *   YARN_INDEX  the same with g falling evenly over the pairs' numbers,
+ *           g = 1 - clamp((i - low) / (high - low), 0, 1), between
+ *           low = max(floor(n(beta_fast)), 0) and
+ *           high = min(ceil(n(beta_slow)), rotary_dim - 1) (low + 0.001 where
+ *           they are equal), n(r) = rotary_dim * ln(original_len / (2pi*r)) /
+ *           (2*ln(base)) being the number of the pair that turns r times over
+ *           the original context
+ * and magnitude 1, or 0.1*ln(factor) + 1 for YARN and YARN_INDEX.  A checkpoint
+ * whose configuration gives beta_fast, beta_slow and an original length was
+ * as a rule trained with YARN_INDEX: at 128 channels, base 1e6, length 32768,
+ * factor 8 and betas of 32 and 1 the two differ by up to a factor of 2.26.
+ * rotary_dim even and >= 2 (>= 4 for NTK), base > 0 (> 1 for YARN_INDEX),
+ * factor >= 1 where it is used, beta_fast > beta_slow (> 0 for YARN_INDEX) and
+ * original_len >= 1 for both, and high >= low for YARN_INDEX. */
 fathom_status fathom_rotary_turns(double *turns, float *magnitude, int32_t rotary_dim, double base,
                                   int32_t scaling, double factor, int64_t original_len,
                                   double beta_fast, double beta_slow);

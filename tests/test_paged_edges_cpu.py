@@ -1,7 +1,9 @@
 """Host side of the calls on a paged cache at the edges of what their documentation allows.  CPU only:
 no call here reaches a kernel."""
 import ctypes
+import math
 
+import numpy as np
 import pytest
 
 import decode_fathom_plan_b200 as fp
@@ -117,3 +119,51 @@ def test_bounds_of_the_lengths_that_a_key_number_cannot_pass_are_refused(lib):
     for longer in (most + 1, 2 ** 31 - 1):
         assert call(longer) == call(longer, most) == fp.FATHOM_ERR_INVALID_ARG
         assert size(c, 1, 1, longer) == size(c, 1, 1, longer, 16) == 0
+
+
+# ------------------------------------------------------------------ rotation over pair numbers
+def yarn_index(rd, base, factor, length, fast, slow):
+    """Radians per position, pair by pair from the formula."""
+    def number(turns):          # of the pair that turns so often over the original context
+        return rd * math.log(length / (2 * math.pi * turns)) / (2 * math.log(base))
+    low, high = max(math.floor(number(fast)), 0), min(math.ceil(number(slow)), rd - 1)
+    if low == high:
+        high += 0.001
+    out = []
+    for i in range(rd // 2):
+        stretched = min(max((i - low) / (high - low), 0.0), 1.0)
+        f = base ** (-2 * i / rd)
+        out.append(f / factor * stretched + f * (1 - stretched))
+    return np.array(out), low, high
+
+
+@pytest.mark.parametrize("rd,base,factor,length,fast,slow", [
+    (128, 1e6, 8.0, 32768, 32.0, 1.0), (64, 1e4, 40.0, 4096, 32.0, 1.0), (128, 5e5, 4.0, 8192, 16.0, 2.0),
+    (2, 1e4, 2.0, 4096, 32.0, 1.0), (128, 1e4, 2.0, 16, 32.0, 1.0), (128, 1e4, 2.0, 10 ** 9, 32.0, 1.0),
+    (96, 1e6, 1.0, 32768, 32.0, 1.0)])
+def test_yarn_over_pair_numbers(lib, rd, base, factor, length, fast, slow):
+    code = fp.RotaryTable._SCALINGS["yarn_index"]
+    got, mag = fp.fathom_rotary_turns(rd, base, code, factor, length, fast, slow)
+    want, _, _ = yarn_index(rd, base, factor, length, fast, slow)
+    assert np.allclose(got.numpy() * 2 * math.pi, want, rtol=1e-12, atol=0)
+    assert abs(mag - (0.1 * math.log(factor) + 1)) <= 2.0 ** -23
+
+
+def test_yarn_over_pair_numbers_worked_by_hand(lib):
+    """128 channels, base 1e6, 32768, betas 32 and 1: n(32) = 128*ln(162.97)/27.63 = 23.6 and
+    n(1) = 128*ln(5215.2)/27.63 = 39.6, so pair 31 is 8/17 of the way from 23 to 40."""
+    got, _ = fp.fathom_rotary_turns(128, 1e6, fp.FATHOM_ROTARY_YARN_INDEX, 8.0, 32768, 32.0, 1.0)
+    f = 1e6 ** (-np.arange(0, 128, 2) / 128)
+    ratio = got.numpy() * 2 * math.pi / f
+    assert np.allclose(ratio[[0, 23, 31, 40, 63]], [1, 1, 9 / 17 + 8 / 17 / 8, 1 / 8, 1 / 8], rtol=1e-12)
+    assert yarn_index(128, 1e6, 8.0, 32768, 32.0, 1.0)[1:] == (23, 40)
+
+
+@pytest.mark.parametrize("args", [(64, 1.0, 4, 2.0, 4096, 32.0, 1.0), (64, 0.5, 4, 2.0, 4096, 32.0, 1.0),
+                                  (64, 1e4, 4, 2.0, 4096, 32.0, 0.0), (64, 1e4, 4, 2.0, 4096, 32.0, -1.0),
+                                  (64, 1e4, 4, 2.0, 0, 32.0, 1.0), (64, 1e4, 4, 0.5, 4096, 32.0, 1.0),
+                                  (64, 1e4, 4, 2.0, 4096, 1.0, 1.0), (64, 1e4, 4, 2.0, 1, 32.0, 1.0),
+                                  (64, 2.0, 4, 2.0, 10 ** 9, 32.0, 1.0), (64, 1e4, 5, 2.0, 4096, 32.0, 1.0)])
+def test_bad_yarn_over_pair_numbers_is_refused(lib, args):
+    with pytest.raises(fp.FathomError):
+        fp.fathom_rotary_turns(*args)

@@ -8,6 +8,7 @@ import torch
 
 import decode_fathom_plan_b200 as fp
 from tests import paged_oracle as po
+from tests.test_paged_edges_cpu import yarn_index
 from tests.test_paged_gpu import BF16, F16, Batch, check, check_rows, few_rows, status
 
 pytestmark = pytest.mark.gpu
@@ -169,3 +170,17 @@ def test_a_key_far_above_the_others_leaves_them_their_weight(lens, prefix, H, dt
         ks, vs = (po.gather(p, b.table[s], np.arange(lens[s]), i, 16) for p in (b.k64, b.v64))
         want, err = po.attend(q[s, i], ks, vs, np.zeros(lens[s]), b.scale, p_step=step, p_tiny=tiny * 2.0 ** -7)
         check(b.out[s, i], want, err + step * np.abs(want) * 1.01 + tiny, (s, i))
+
+
+def test_rows_turned_by_yarn_over_pair_numbers():
+    T, h, d = 37, 3, 128
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn([T, h, d], generator=g).to(BF16).cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 5003
+    out = torch.empty([T, h, d], dtype=torch.float32, device="cuda")
+    tab = fp.RotaryTable(d, base=1e6, scaling="yarn_index", factor=8.0, original_len=32768)
+    fp.fathom_qk_norm_rope(x, None, pos, out, None, tab)
+    freq, _, _ = yarn_index(d, 1e6, 8.0, 32768, 32.0, 1.0)
+    y, size = po.norm_rope(po.f64(x), pos.cpu().numpy().astype(np.float64), None, 1e-6, freq,
+                           0.1 * math.log(8.0) + 1.0)
+    check(out, y, po.norm_rope_tolerance(y, size, torch.float32))
