@@ -597,12 +597,36 @@ class RotaryTable:
             raise ValueError(f"scaling is one of {', '.join(self._SCALINGS)}, not {scaling!r}")
         turns, magnitude = fathom_rotary_turns(rotary_dim, base, self._SCALINGS[scaling], factor,
                                                original_len, beta_fast, beta_slow)
+        self._set(turns, interleaved, magnitude, device)
+
+    @classmethod
+    def from_frequencies(cls, frequencies, head_dim: int, interleaved: bool = False,
+                         magnitude: float = 1.0, device: Optional[int] = None):
+        """A table of given frequencies, radians per position of each pair
+        (numbers or a tensor [rotary_dim/2], kept in float64), for scalings
+        that fathom_rotary_turns does not have."""
+        import math
+
+        import torch
+        f = torch.as_tensor(frequencies, dtype=torch.float64).detach().cpu()
+        if f.dim() != 1 or not 1 <= f.numel() <= head_dim // 2:
+            raise ValueError(f"1 to {head_dim // 2} frequencies are wanted for a head of {head_dim} "
+                             f"channels, not {list(f.shape)}")
+        if not torch.isfinite(f).all() or not math.isfinite(magnitude):
+            raise ValueError("finite frequencies and magnitude are wanted")
+        self = cls.__new__(cls)
+        self._set(f / (2 * math.pi), interleaved, float(magnitude), device)
+        return self
+
+    def _set(self, turns, interleaved, magnitude, device):
+        import torch
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else device)
         self.turns = turns.to(self.device)
         self.magnitude = magnitude
         self.device_index = self.device.index
-        self.desc = fathom_rotary(self.turns.data_ptr(), rotary_dim, int(interleaved), magnitude)
+        self.desc = fathom_rotary(self.turns.data_ptr(), 2 * turns.numel(), int(interleaved),
+                                  magnitude)
 
 
 class PagedKV:

@@ -167,3 +167,11 @@ def test_yarn_over_pair_numbers_worked_by_hand(lib):
 def test_bad_yarn_over_pair_numbers_is_refused(lib, args):
     with pytest.raises(fp.FathomError):
         fp.fathom_rotary_turns(*args)
+
+
+@pytest.mark.parametrize("freq", [[], [1.0] * 33, [[1.0]], [math.nan], [1.0, math.inf]])
+def test_bad_frequencies_are_refused(freq):
+    with pytest.raises(ValueError):
+        fp.RotaryTable.from_frequencies(freq, 64)
+    with pytest.raises(ValueError):
+        fp.RotaryTable.from_frequencies([1.0], 64, magnitude=math.inf)

@@ -184,3 +184,20 @@ def test_rows_turned_by_yarn_over_pair_numbers():
     y, size = po.norm_rope(po.f64(x), pos.cpu().numpy().astype(np.float64), None, 1e-6, freq,
                            0.1 * math.log(8.0) + 1.0)
     check(out, y, po.norm_rope_tolerance(y, size, torch.float32))
+
+
+@pytest.mark.parametrize("rd,inter", [(64, False), (48, True), (2, False)])
+def test_rows_turned_by_given_frequencies(rd, inter):
+    T, h, d = 9, 2, 64
+    g = torch.Generator().manual_seed(rd)
+    x = torch.randn([T, h, d], generator=g).cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 1009
+    freq = torch.rand([rd // 2], generator=g, dtype=torch.float64) * 3 - 1      # any, negative ones too
+    tab = fp.RotaryTable.from_frequencies(freq, d, inter, 1.25)
+    out = torch.empty_like(x)
+    fp.fathom_qk_norm_rope(x, None, pos, out, None, tab)
+    y, size = po.norm_rope(po.f64(x), pos.cpu().numpy().astype(np.float64), None, 1e-6, freq.numpy(), 1.25, inter)
+    check(out, y, po.norm_rope_tolerance(y, size, torch.float32))
+    same = fp.RotaryTable(d, rd, 1e4, inter)
+    again = fp.RotaryTable.from_frequencies([1e4 ** (-2 * i / rd) for i in range(rd // 2)], d, inter)
+    assert torch.allclose(same.turns, again.turns, rtol=1e-14, atol=0)
