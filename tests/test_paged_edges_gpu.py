@@ -201,3 +201,45 @@ def test_rows_turned_by_given_frequencies(rd, inter):
     same = fp.RotaryTable(d, rd, 1e4, inter)
     again = fp.RotaryTable.from_frequencies([1e4 ** (-2 * i / rd) for i in range(rd // 2)], d, inter)
     assert torch.allclose(same.turns, again.turns, rtol=1e-14, atol=0)
+
+
+# ------------------------------------------------------------- bfloat16 probabilities in two terms
+@pytest.mark.parametrize("lens", [[16], [1024, 48], [700]])
+@pytest.mark.parametrize("G,d", [(4, 128), (8, 64), (1, 96), (3, 256)])
+def test_bfloat16_probabilities_of_own_keys_keep_sixteen_bits(lens, G, d):
+    """Of every 16 keys one has the largest weight, 1, and 15 a weight that bfloat16 rounds badly;
+    their values all but cancel, so that the rounding of the output hides nothing.
+
+    What one term leaves of a weight is at most 2^-8 of it, what the second leaves of that 2^-16."""
+    H, page = 2, 16
+    b = Batch(lens, 0, H, G, d, page, BF16, False, 3)
+    scores = torch.arange(-256, 0).to(BF16).unique()[:-1] / 64
+    weights = torch.exp(scores.double())
+    off = (weights.float().to(BF16).double() - weights).abs() / weights
+    at = int(off.argmax())
+    weight = float(weights[at])
+    top = float(torch.tensor(-15 * weight).to(BF16))            # value of the largest, against 15 ones
+    k, v = torch.zeros_like(b.kv.k), torch.ones_like(b.kv.v)
+    k[..., 0] = float(scores[at])
+    k[:, :, 5, 0] = 0.0                                         # one slot of each page of 16
+    v[:, :, 5] = top
+    b.kv.k.copy_(k)
+    b.kv.v.copy_(v)
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.scale = 1.0
+    b.attention()
+    assert status() == fp.FATHOM_OK
+    for s, n in enumerate(lens):
+        j = np.arange(n)
+        ks, vs = np.zeros((n, d)), np.ones((n, d))
+        ks[:, 0] = np.where(j % page == 5, 0.0, float(scores[at]))
+        vs[j % page == 5] = top
+        want, err = po.attend(po.f64(b.q)[s, 0], ks, vs, np.zeros(n), 1.0, p_step=2.0 ** -16)
+        tol = err + po.HALF_STEP[BF16] * np.abs(want) * 1.01
+        # a weight in one term alone would be seen
+        p = np.exp(ks[:, 0])
+        one = torch.from_numpy(p).float().to(BF16).double().numpy() @ vs / p.sum()
+        assert (np.abs(one - want) > 4 * tol).all()
+        for i in range(H * G):
+            check(b.out[s, i], want, tol, (s, i))
