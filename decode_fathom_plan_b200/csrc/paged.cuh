@@ -112,11 +112,14 @@ __device__ __forceinline__ float exp2_fast(float x)
 }
 
 // A dot product as a logit times log2(e), so that the softmax is a power of
-// two.  The cap is cap * tanh(x / cap) with tanh(y) = 1 - 2 / (1 + e^2y): its
-// error is some 2^-23 of the cap, an absolute one of a logit; the hardware's
-// own tanh is 2^-11 off, 0.02 of a logit at a cap of 50.  Larger caps than
-// kMaxSoftcap, where the error is 2^-8 of a logit at most (half a step of a
-// bfloat16 probability), are refused.
+// two.  The cap is cap * tanh(x / cap) with tanh(y) = 1 - 2 / (1 + e^2y), off by
+// at most 2^-20 of the cap, an absolute error of a logit: in units of 2^-23 the
+// power's 2^-22 counts 1 (the quotient q <= 2 moves by q (1 - q/2) <= 1/2 of
+// it), four roundings of its argument 0.9, that of 1 + e^2y 1, the quotient's
+// two last places 2, the product and the constant's rounding 1: 5.9 in all
+// (worst measured over 2^24 scores 2.5, 2^-21.6 of the cap).  The hardware's own
+// tanh is 2^-11 off, 0.02 of a logit at a cap of 50.  Caps larger than
+// kMaxSoftcap, at which that bound is 2^-6 of a logit, are refused.
 constexpr float kMaxSoftcap = 16384.0f;
 struct ScoreArgs {
     float scale;      // softmax_scale * log2(e); with a cap 2 * log2(e) * softmax_scale / cap
@@ -158,9 +161,12 @@ __device__ __forceinline__ void store_row(const PagedQuery &q, int b, int head, 
 // ------------------------------------------------- kernels that follow closely
 // A kernel launched by launch_overlapped may start once every CTA of the one
 // before it in the stream has called let_next_kernel_start() or ended; what it
-// reads or overwrites of that kernel, or of those before it, it touches after
-// wait_for_earlier_kernels(), which waits for them to end.  (So a kernel that
-// lets the next one start does it after its own wait.)  All that is gained is
+// reads or overwrites of that kernel it touches after wait_for_earlier_kernels(),
+// which waits for it to end.  A kernel lets the next one start after its own
+// wait: then all that was in the stream before the kernel has ended.  On that
+// rests the one exception, the kernel of the own keys behind a prefix: it takes
+// nothing from the kernel of the prefix and runs beside it, without a wait but
+// at its end, so that whoever waits for it waits for both.  All that is gained is
 // the launch: a microsecond or two from one small kernel to the next.
 __device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

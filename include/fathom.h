@@ -393,7 +393,8 @@ fathom_status fathom_sparse_attention(const float *keys, const float *values, in
  * CUDA graph (make the first call of a kind, which may load its device code,
  * before a capture), allocate nothing and make no host synchronisation.  Their
  * kernels are launched while the kernel before them in the stream ends
- * (programmatic stream serialization) and touch no memory before it has. */
+ * (programmatic stream serialization), and touch no memory before all that a
+ * call finds in the stream has ended. */
 
 /* Element types of rows and caches. */
 typedef enum {
@@ -539,11 +540,12 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  * query head i = h*G + g of sequence b with n = seq_lens[b] keys,
  *   s_j = softmax_scale * (q[b][i] . K_j),
  *   s_j = softcap * tanh(s_j / softcap)     where softcap > 0 (at most 16384;
- *                                           within 2^-22 * softcap),
+ *                                           within 2^-20 * softcap),
  *   s_j = s_j - slopes[i] * (n - 1 - j)     where slopes is not NULL
  *                                           (the query stands at n - 1),
  *   out[b][i] = sum_j softmax(s)_j V_j,  j in [0, n).
- * A sequence of length 0 (a padded batch row) gets zeros.
+ * A sequence of length 0 (a padded batch row) gets zeros, and so does a row
+ * all of whose scores are -inf.
  * prefix_len > 0 states that the first prefix_len keys (a multiple of
  * page_size) are the same pages in the table's row of every sequence that has
  * keys: they are looked up in one such row and multiplied with the queries of
@@ -558,9 +560,12 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  * q, out: rows of n_seqs tokens with G*n_kv_heads heads, in the cache's type,
  * 16-byte aligned, strides positive multiples of 8, n_seqs at most 65535; G
  * 1..8.  slopes: device float32
- * [G*n_kv_heads].  Scores, softmax and sums are float32; each probability is
- * rounded to the cache's type for its product with V, which is accumulated in
- * float32.  workspace: device memory that no other call in flight uses. */
+ * [G*n_kv_heads].  Scores, softmax and sums are float32; for its product with
+ * V, which is accumulated in float32, a probability is rounded to the cache's
+ * type: float16 once, to 11 bits and 2^-32 of the row's largest; bfloat16 to two
+ * terms (16 bits), but over a shared prefix to one (8 bits) where the batch's
+ * repeated reads of it, 4 * head_dim * n_kv_heads * prefix_len * (n_seqs - 1)
+ * bytes, pass 8 MiB.  prefix_len 0 keeps both terms.  workspace: device memory that no other call in flight uses. */
 fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_rows *q,
                                      const int32_t *page_table, int32_t table_stride,
                                      const int32_t *seq_lens, int32_t n_seqs, int32_t max_len,
