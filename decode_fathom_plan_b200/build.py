@@ -4,7 +4,9 @@ Each translation unit is compiled to an object under _build/ (in parallel),
 then linked into decode_fathom_plan_b200/libfathom.so.  _binding.so is the
 Python module that passes torch tensors to the library's calls on a paged
 cache (csrc/binding.cpp).  Each is rebuilt only when a source or header is
-newer than it.
+newer than it, the module also when torch is another than it was built for.
+The library needs neither torch nor its headers: where they are missing it is
+built alone, and the calls that take tensors of a paged cache raise.
 """
 from __future__ import annotations
 
@@ -51,12 +53,43 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def torch_mark() -> bytes:
+    """What _binding.so holds of the torch that it was built for (empty: none here)."""
+    from importlib import metadata
+    try:
+        return ("built for torch " + metadata.version("torch") + ";").encode()
+    except metadata.PackageNotFoundError:
+        return b""
+
+
 def binding_up_to_date() -> bool:
     if not os.path.exists(BINDING):
         return False
     t = os.path.getmtime(BINDING)
+    with open(BINDING, "rb") as f:
+        if torch_mark() not in f.read():
+            return False
     return all(os.path.getmtime(p) <= t for p in
                [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def binding_lacks() -> str:
+    """What this machine lacks to build _binding.so; empty where it has all."""
+    import sysconfig
+    if not torch_mark():
+        return "torch is not installed"
+    from torch.utils import cpp_extension
+    dirs = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+    for header in ("torch/csrc/autograd/python_variable.h", "Python.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in dirs):
+            return header + " is missing"
+    if not shutil.which(cxx()):
+        return cxx() + " is missing"
+    return ""
+
+
+def cxx() -> str:
+    return os.environ.get("CXX") or "g++"
 
 
 def build_binding(verbose: bool = False):
@@ -70,8 +103,8 @@ def build_binding(verbose: bool = False):
         cpp_extension.include_paths()
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
-           "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + \
+    cmd = [cxx(), "-O2", "-std=c++17", "-fPIC",
+           "-shared", '-DFATHOM_TORCH_MARK="%s"' % torch_mark().decode(), "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + \
         [x for i in includes for x in ("-isystem", i)] + [BINDING_SRC, "-o", tmp, "-L" + PKG,
          "-l:libfathom.so", "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
@@ -86,7 +119,13 @@ def build_binding(verbose: bool = False):
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     build_library(force, verbose, ptxas_info)
     if force or not binding_up_to_date():
-        build_binding(verbose)
+        lacks = binding_lacks()
+        if lacks:
+            if os.path.exists(BINDING):          # of another source or torch: not to be loaded
+                os.remove(BINDING)
+            print(f"{BINDING} is not built: {lacks}", file=sys.stderr)
+        else:
+            build_binding(verbose)
     return LIB
 
 

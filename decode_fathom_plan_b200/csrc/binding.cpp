@@ -325,7 +325,7 @@ PyMethodDef methods[] = {
     {"sparse_attention_paged", (PyCFunction)(void *)sparse_attention_paged, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", FATHOM_TORCH_MARK, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

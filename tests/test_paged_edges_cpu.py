@@ -175,3 +175,28 @@ def test_bad_frequencies_are_refused(freq):
         fp.RotaryTable.from_frequencies(freq, 64)
     with pytest.raises(ValueError):
         fp.RotaryTable.from_frequencies([1.0], 64, magnitude=math.inf)
+
+
+# -------------------------------------------------------------------------- the native module
+def test_module_is_rebuilt_for_another_torch(lib, monkeypatch):
+    assert fbuild.binding_up_to_date() and not fbuild.binding_lacks()
+    monkeypatch.setattr(fbuild, "torch_mark", lambda: b"built for torch 0.0.0;")
+    assert not fbuild.binding_up_to_date()
+
+
+@pytest.mark.parametrize("lack", ["torch", "headers", "compiler"])
+def test_library_is_built_where_the_module_cannot_be(lib, monkeypatch, tmp_path, capsys, lack):
+    from torch.utils import cpp_extension
+    stale = tmp_path / "_binding.so"
+    stale.write_bytes(b"of another torch")
+    monkeypatch.setattr(fbuild, "BINDING", str(stale))
+    if lack == "torch":
+        monkeypatch.setattr(fbuild, "torch_mark", lambda: b"")
+        stale.unlink()
+    elif lack == "headers":
+        monkeypatch.setattr(cpp_extension, "include_paths", lambda *a, **k: [str(tmp_path)])
+    else:
+        monkeypatch.setenv("CXX", "no-such-compiler")
+    assert fbuild.build() == fbuild.LIB
+    assert "is not built" in capsys.readouterr().err
+    assert not stale.exists()
