@@ -54,7 +54,6 @@ constexpr int kTile = 128;                       // keys of a tile
 constexpr int kStep = 64;                        // keys of a product
 constexpr int kBlockBytes = kTile * 128;         // 128 rows of 64 channels (128 bytes, swizzled)
 constexpr unsigned long long kSettleNs = 500000000ull;  // for what is under way after a stop
-constexpr unsigned long long kTryNs = 100000ull;        // that one try of a wait may last
 constexpr int kTmemCols = 512;
 constexpr int kStageBytes = 4 * 32 * 128;        // 32 channels of a slot's rows in float32
 
@@ -100,11 +99,12 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-// Whether the phase of the given parity is over; waits up to ns for it, where that is 0 not at all.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t ns)
+// Whether the phase of the given parity is over; waits for it a while (the hardware's own limit: one
+// given with the instruction cost 0.5% with 64 agents), or not at all.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, bool linger = true)
 {
     uint32_t ok;
-    if (ns == 0)
+    if (!linger)
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
             " selp.u32 %0, 1, 0, p;\n}\n"
@@ -113,10 +113,10 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
             " selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(ns)
+            : "r"(bar), "r"(parity)
             : "memory");
     return ok != 0;
 }
@@ -131,8 +131,7 @@ __device__ __forceinline__ unsigned long long global_ns()
 // issue products and copies make no calls.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *stop, unsigned long long limit)
 {
-    const uint32_t once = (uint32_t)(limit < kTryNs ? limit : kTryNs);
-    bool ok = mbar_try(bar, parity, once);
+    bool ok = mbar_try(bar, parity, limit > 0);
     if (!ok) {
         const unsigned long long start = global_ns();
         do {
@@ -140,7 +139,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
                 *stop = 1;
                 break;
             }
-            ok = mbar_try(bar, parity, once);
+            ok = mbar_try(bar, parity);
         } while (!ok);
     }
     return __all_sync(0xFFFFFFFFu, ok);
@@ -149,7 +148,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void wait_anyway(uint32_t bar, uint32_t parity)
 {
     const unsigned long long start = global_ns();
-    while (!mbar_try(bar, parity, (uint32_t)kTryNs) && global_ns() - start < kSettleNs) {
+    while (!mbar_try(bar, parity) && global_ns() - start < kSettleNs) {
     }
     __syncwarp();
 }
@@ -354,18 +353,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             const int key = (t0 + tile) * kTile + lane * box;
             return lane < boxes && key < a.prefix_len ? table[key >> shift] : a.n_pages;
         };
-        int page = page_of(0);                                  // mostly that row: beside the lengths
-        int from = -1;
-        for (int s = 0; s < a.seqs && from < 0; s += 32) {
-            const int n = s + lane < a.seqs ? a.q.seq_lens[s + lane] : 0;
-            const unsigned in = __ballot_sync(0xFFFFFFFFu, n > 0 && !refused_length(n, a.prefix_len, a.max_len));
-            if (in) from = s + __ffs(in) - 1;
-        }
-        const int keys_end = from < 0 ? 0 : a.prefix_len;       // with no sequence, no page is looked at
-        if (from > 0) {
-            table += (size_t)from * a.table_stride;
-            page = page_of(0);
-        }
+        const auto length_of = [&](int s) { return s < a.seqs ? a.q.seq_lens[s] : 0; };
+        int page = page_of(0), len = length_of(lane);           // mostly it is the first row
         __syncwarp();
         if (elect_one()) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -387,6 +376,18 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             __syncwarp();
         } else {
             asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory");
+        }
+        // which row it is, once the first copies that need none are on their way
+        int from = -1;
+        for (int s = 0; s < a.seqs && from < 0; s += 32) {
+            if (s > 0) len = length_of(s + lane);
+            const unsigned in = __ballot_sync(0xFFFFFFFFu, len > 0 && !refused_length(len, a.prefix_len, a.max_len));
+            if (in) from = s + __ffs(in) - 1;
+        }
+        const int keys_end = from < 0 ? 0 : a.prefix_len;       // with no sequence, no page is used
+        if (from > 0) {
+            table += (size_t)from * a.table_stride;
+            page = page_of(0);
         }
         Place<kStages> at;
         bool ok = true, bad = false;
