@@ -583,7 +583,8 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
 #pragma unroll
                 for (int k = 4; k < kStep; ++k) tops[k & 3] = fmaxf(tops[k & 3], x[k]);
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mult;
-                if (__any_sync(0xFFFFFFFFu, top > m + kRescale)) {
+                // rows of no sequence have no vote: behind the slot's last, Q is whatever lay in shared memory
+                if (__any_sync(0xFFFFFFFFu, mine && top > m + kRescale)) {
                     const float next = fmaxf(m, top);
                     const float w = m == next ? 1.0f : exp2_fast(m - next);
                     m = next;

@@ -243,3 +243,27 @@ def test_bfloat16_probabilities_of_own_keys_keep_sixteen_bits(lens, G, d):
         assert (np.abs(one - want) > 4 * tol).all()
         for i in range(H * G):
             check(b.out[s, i], want, tol, (s, i))
+
+
+# --------------------------------------------------- sums that nothing but the inputs decides
+@pytest.mark.parametrize("G,d,dtype", [(3, 128, BF16), (5, 128, BF16), (6, 64, F16), (7, 256, BF16), (5, 192, F16)])
+def test_sums_do_not_depend_on_what_ran_before(G, d, dtype):
+    """A slot of 128 rows holds 128 / G whole sequences; behind them lies what another kernel left in
+    shared memory, which must not decide when the other rows of a warp renew their maximum."""
+    prefix, H = 2048, 2
+    bs = [shared([prefix + 40 + i for i in range(2 * (128 // G) + 3)], dtype, prefix, H, G, d, seed=60 + i)
+          for i in range(2)]
+    bs[1].q.mul_(40)                                            # leaves large rows behind
+    bs[1].kv.k.mul_(4)
+    want = None
+    for _ in range(12):
+        for b in bs:
+            b.attention(ws=getattr(b, "ws", None))
+        want = bs[0].out.clone() if want is None else want
+        assert torch.equal(bs[0].out, want)
+        bs[0].out.fill_(math.nan)
+        torch.cuda.synchronize()
+        bs[0].attention(ws=bs[0].ws)
+        assert torch.equal(bs[0].out, want)
+    assert status() == fp.FATHOM_OK
+    check_rows(bs[0], few_rows(bs[0], 4))
