@@ -267,3 +267,104 @@ def test_sums_do_not_depend_on_what_ran_before(G, d, dtype):
         assert torch.equal(bs[0].out, want)
     assert status() == fp.FATHOM_OK
     check_rows(bs[0], few_rows(bs[0], 4))
+
+
+# ------------------------------------------------------------------ calls that follow one another
+@pytest.mark.parametrize("lens,H,G,d", [([2048 + 40 + 11 * i for i in range(9)], 8, 4, 64),
+                                        ([1024 + 600 + i for i in range(33)], 2, 5, 128)])
+def test_attention_reads_what_the_call_before_it_wrote(lens, H, G, d):
+    """The kernel of the own keys starts beside that of the prefix: keys, lengths and pages that were
+    written just before are the new ones, with and without a wait of the host in between."""
+    n, prefix = len(lens), lens[0] // 1024 * 1024
+    b = shared(lens, BF16, prefix, H, G, d)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ks = torch.randn([40, n, H, d], generator=g, device="cuda").to(BF16)
+    qs = torch.randn([40, n, H * G, d], generator=g, device="cuda").to(BF16)
+    seq = torch.arange(n, dtype=torch.int32, device="cuda")
+    full, table = b.lens_t.clone(), b.table_t.clone()
+    b.attention()
+
+    start = b.kv.k.clone(), b.kv.v.clone()
+
+    def steps(wait):
+        outs = []
+        b.kv.k.copy_(start[0])
+        b.kv.v.copy_(start[1])
+        for i in range(40):
+            pos = full - 1 - i % 7
+            fp.fathom_append_kv(b.kv.desc, ks[i], ks[39 - i], seq, pos, table)
+            if wait:
+                torch.cuda.synchronize()
+            b.q = qs[i]
+            torch.add(pos, 1, out=b.lens_t)                     # a kernel of another library before the call
+            b.attention(max_len=max(lens), ws=b.ws)
+            fp.fathom_append_kv(b.kv.desc, ks[39 - i], ks[i], seq, pos, table)   # and one that overwrites after it
+            b.attention(max_len=max(lens), ws=b.ws)
+            outs.append(b.out.clone())
+            if wait:
+                torch.cuda.synchronize()
+        return torch.stack(outs)
+
+    first = steps(True)
+    for _ in range(5):
+        assert torch.equal(steps(False), first)
+    assert status() == fp.FATHOM_OK
+
+
+def test_the_whole_step_captured_and_replayed():
+    """Norm, rotation, append, plan, scan, and both attentions as one graph."""
+    H, G, d, page, n, k = 2, 4, 128, 16, 4000, 256
+    hq = H * G
+    g = torch.Generator(device="cuda").manual_seed(9)
+    kv = fp.PagedKV(n // page + 2, page, H, d)
+    kv.k.copy_(torch.randn(kv.k.shape, generator=g, device="cuda"))
+    kv.v.copy_(torch.randn(kv.v.shape, generator=g, device="cuda"))
+    table = torch.randperm(n // page + 1, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    ix = fp.KeyIndex(H, G, n, d)
+    ix.pack(torch.randn([H, n, d], generator=g, device="cuda"))
+    buf = fp.ScanBuffers(ix, k)
+    rot = fp.RotaryTable(d, base=1e6)
+    w = torch.ones(d, dtype=BF16, device="cuda")
+    qkv = torch.empty([1, hq + 2 * H, d], dtype=BF16, device="cuda")
+    pos, lens, seq = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(3))
+    q = torch.empty([1, hq, d], dtype=BF16, device="cuda")
+    k32 = torch.empty([1, H, d], device="cuda")
+    some, every = torch.empty_like(q), torch.empty_like(q)
+    budget = torch.full([hq], 2 * d, dtype=torch.int32, device="cuda")
+    ws, ws2 = (torch.empty(1 << 22, dtype=torch.uint8, device="cuda") for _ in range(2))
+
+    def step():
+        fp.fathom_qk_norm_rope(qkv[:, :hq], qkv[:, hq:hq + H], pos, q, k32, rot, w, w)
+        fp.fathom_append_kv(kv.desc, qkv[:, hq:hq + H], qkv[:, hq + H:], seq, pos, table, rot, w)
+        fp.plan_and_scan(ix, q.view(hq, d).view(torch.int16), budget, buf)
+        fp.fathom_sparse_attention_paged(kv.desc, q, buf.idx[None], table, lens, some, ws, d ** -0.5)
+        fp.fathom_paged_attention(kv.desc, q, table, lens, n + page, every, ws2, d ** -0.5)
+
+    def inputs(i):
+        qkv.copy_(torch.randn(qkv.shape, generator=torch.Generator(device="cuda").manual_seed(i), device="cuda"))
+        pos.fill_(n - 20 + i)
+        lens.fill_(n - 19 + i)
+
+    inputs(0)
+    lens.fill_(n)
+    step()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+        step()
+        graph.capture_end()
+    for i in range(6):
+        inputs(i)
+        lens.fill_(n)
+        for out in (some, every, q, k32):
+            out.fill_(math.nan)
+        step()
+        want = [x.clone() for x in (q, k32, some, every, kv.k, buf.idx)]
+        for out in (some, every, q, k32):
+            out.fill_(math.nan)
+        graph.replay()
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip((q, k32, some, every, kv.k, buf.idx), want))
+        assert torch.isfinite(some).all() and torch.isfinite(every).all()
+    assert status() == fp.FATHOM_OK
