@@ -368,3 +368,100 @@ def test_the_whole_step_captured_and_replayed():
         assert all(torch.equal(x, y) for x, y in zip((q, k32, some, every, kv.k, buf.idx), want))
         assert torch.isfinite(some).all() and torch.isfinite(every).all()
     assert status() == fp.FATHOM_OK
+
+
+# ------------------------------------------------------------- layouts and sizes at their ends
+@pytest.mark.parametrize("prefix", [0, 2048])
+@pytest.mark.parametrize("q_heads_first,out_heads_first", [(False, True), (True, False)])
+@pytest.mark.parametrize("G,d,dtype", [(4, 128, BF16), (3, 96, F16), (1, 256, BF16)])
+def test_attention_on_views(prefix, q_heads_first, out_heads_first, G, d, dtype):
+    """Queries inside a projection or stored head by head, outputs likewise, keys and values of several
+    layers side by side in one pool."""
+    H, page, lens = 4, 16, [prefix + 5, 0, prefix + 77, prefix + 1, prefix + 16] + [prefix + 30] * 9
+    b = Batch(lens, prefix, H, G, d, page, dtype, False, 70)
+    n, hq = len(lens), H * G
+    pool = torch.full([b.kv.k.shape[0], 3, page, 2, H, d + 32], math.nan, dtype=dtype, device="cuda")
+    k, v = (pool[:, 1, :, i, :, :d].transpose(1, 2) for i in range(2))
+    k.copy_(b.kv.k)
+    v.copy_(b.kv.v)
+    b.kv = fp.PagedKV.from_tensors(k, v)
+
+    def rows(heads_first):
+        if heads_first:
+            return torch.full([hq + 1, n, d], math.nan, dtype=dtype, device="cuda")[1:].transpose(0, 1)
+        return torch.full([n, hq + 2 * H, d + 8], math.nan, dtype=dtype, device="cuda")[:, 1:1 + hq, :d]
+    q, out = rows(q_heads_first), rows(out_heads_first)
+    q.copy_(b.q)
+    b.q, b.out = q, out
+    b.attention()
+    assert status() == fp.FATHOM_OK
+    at = {(s, i) for s in (0, 1, 2, n - 1) for i in (0, hq - 1)}
+    check_rows(b, at)
+    idx = np.full((n, hq, 40), -1, np.int32)
+    for s, m in enumerate(lens):
+        if m:
+            idx[s] = np.random.default_rng(s).integers(0, m, (hq, 40))
+    ws = torch.empty(max(16, fp.fathom_sparse_attention_paged_workspace_bytes(n, hq, d, 40)), dtype=torch.uint8,
+                     device="cuda")
+    fp.fathom_sparse_attention_paged(b.kv.desc, b.q, torch.from_numpy(idx).cuda(), b.table_t, b.lens_t, b.out, ws,
+                                     b.scale)
+    want, tol = b.expect(idx=idx, rows=at, round_p=False)
+    where = tuple(np.array(sorted(at)).T)
+    check(b.out.cpu()[where], want[where], tol[where])
+
+
+@pytest.mark.parametrize("n,H,G,prefix", [(65535, 1, 1, 0), (65535, 1, 1, 8), (3001, 2, 5, 64), (2, 700, 8, 512)])
+def test_largest_batches_and_most_heads(n, H, G, prefix):
+    d, page = 32, 8
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in np.where(rng.random(n) < 0.2, 0, prefix + rng.integers(1, 20, n))]
+    lens[-1] = prefix + 19
+    b = Batch(lens, prefix, H, G, d, page, BF16, False, 71)
+    b.attention()
+    assert status() == fp.FATHOM_OK
+    hq = H * G
+    at = {(int(s), int(i)) for s, i in zip(rng.integers(0, n, 40), rng.integers(0, hq, 40))} | {(0, 0), (n - 1, hq - 1)}
+    check_rows(b, at)
+    empty = torch.tensor(lens, device="cuda") == 0
+    assert (b.out[empty] == 0).all()
+    k = 5
+    idx = np.where(np.array(lens)[:, None, None] > 0, rng.integers(0, np.maximum(lens, 1)[:, None, None], (n, hq, k)),
+                   -1).astype(np.int32)
+    ws = torch.empty(fp.fathom_sparse_attention_paged_workspace_bytes(n, hq, d, k), dtype=torch.uint8, device="cuda")
+    b.out.fill_(math.nan)
+    fp.fathom_sparse_attention_paged(b.kv.desc, b.q, torch.from_numpy(idx).cuda(), b.table_t, b.lens_t, b.out, ws,
+                                     b.scale)
+    want, tol = b.expect(idx=idx, rows=at, round_p=False)
+    where = tuple(np.array(sorted(at)).T)
+    check(b.out.cpu()[where], want[where], tol[where])
+    assert status() == fp.FATHOM_OK and (b.out[empty] == 0).all()
+
+
+def test_a_sequence_of_more_keys_than_a_float_counts():
+    """17 million keys, 8 queries, a bias by distance; the same keys selected by a list of their ends."""
+    n, G, d, page = (1 << 24) + 300001, 8, 32, 1024
+    pages = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kv = fp.PagedKV(pages, page, 1, d)
+    for x in (kv.k, kv.v):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda", dtype=BF16))
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    q = torch.randn([1, G, d], generator=g, device="cuda").to(BF16)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    slopes = torch.tensor([0.0, 0.0, 1e-6, 1e-5, 1e-4, 0.01, 1.0, 0.0], device="cuda")
+    ws = torch.empty(fp.fathom_paged_attention_workspace_bytes(kv.desc, 1, G, n), dtype=torch.uint8, device="cuda")
+    fp.fathom_paged_attention(kv.desc, q, table, lens, n, out, ws, d ** -0.5, slopes=slopes)
+    assert status() == fp.FATHOM_OK
+    j = torch.arange(n, device="cuda")
+    at = table[0].long()[j // page] * page + j % page
+    keys, values = (x.reshape(-1, d)[at].double() for x in (kv.k, kv.v))
+    dist = (n - 1 - j).double()
+    for i in range(G):
+        s = keys @ q[0, i].double() * d ** -0.5 - slopes[i].double() * dist
+        p = torch.exp(s - s.max())
+        want, size = p @ values / p.sum(), p @ values.abs() / p.sum()
+        # scores of up to 6 and biases, each to 2^-17 and 2^-21 of itself where the weight is (within 20
+        # of the largest), two-term probabilities, the rounding of the output
+        tol = size * (6 * 2.0 ** -17 + 2.0 ** -19 + 2.0 ** -16 + 26 * 2.0 ** -21) + want.abs() * 2.0 ** -8
+        check(out[0, i], want.cpu().numpy(), tol.cpu().numpy(), i)
