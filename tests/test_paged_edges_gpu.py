@@ -465,3 +465,48 @@ def test_a_sequence_of_more_keys_than_a_float_counts():
         # of the largest), two-term probabilities, the rounding of the output
         tol = size * (6 * 2.0 ** -17 + 2.0 ** -19 + 2.0 ** -16 + 26 * 2.0 ** -21) + want.abs() * 2.0 ** -8
         check(out[0, i], want.cpu().numpy(), tol.cpu().numpy(), i)
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    T, h, d, far = 4, 2, 64, 1 << 30
+    pool = torch.empty(3 * far + h * d, dtype=BF16, device="cuda")
+    x = pool.as_strided([T, h, d], [far, d, 1])
+    g = torch.Generator().manual_seed(3)
+    src = torch.randn([T, h, d], generator=g).to(BF16)
+    w = (1 + torch.rand([d], generator=g)).to(BF16).cuda()
+    pos = torch.tensor([5, 2 ** 20, 0, 77], dtype=torch.int32, device="cuda")
+    tab = fp.RotaryTable(d, base=1e6)
+    y, size = po.norm_rope(po.f64(src), pos.cpu().numpy().astype(np.float64), po.f64(w), 1e-6, po.turns(d, 1e6)[0])
+    tol = po.norm_rope_tolerance(y, size, BF16)
+    x.copy_(src)
+    near = torch.empty([T, h, d], dtype=BF16, device="cuda")
+    fp.fathom_qk_norm_rope(x, None, pos, near, None, tab, w)
+    check(near, y, tol)
+    fp.fathom_qk_norm_rope(None, x, pos, None, x, tab, None, w)             # in place, far apart
+    check(x, y, tol)
+    x.copy_(src)
+    kv = fp.PagedKV(2, 8, h, d)
+    seq = torch.zeros(T, dtype=torch.int32, device="cuda")
+    slot = torch.arange(T, dtype=torch.int32, device="cuda") * 3
+    fp.fathom_append_kv(kv.desc, x, x, seq, slot, torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"), None, w)
+    y, size = po.norm_rope(po.f64(src), None, po.f64(w))
+    for t in range(T):
+        at = int(slot[t])
+        check(kv.k[1 - at // 8, :, at % 8], y[t], po.norm_rope_tolerance(y, size, BF16)[t])
+        assert torch.equal(kv.v[1 - at // 8, :, at % 8].cpu(), src[t])
+    assert status() == fp.FATHOM_OK
+
+
+@pytest.mark.parametrize("T,hq,hk,d,dtype", [(1, 65535, 1, 32, BF16), (3, 1, 4097, 96, F16), (70001, 1, 1, 32, BF16)])
+def test_norm_rope_of_most_heads_and_tokens(T, hq, hk, d, dtype):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q, k = (torch.randn([T, n, d], generator=g, device="cuda").to(dtype) for n in (hq, hk))
+    w = (1 + torch.rand([d], generator=g, device="cuda")).to(dtype)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 11
+    q_out, k_out = torch.full_like(q, math.nan), torch.full([T, hk, d], math.nan, device="cuda")
+    fp.fathom_qk_norm_rope(q, k, pos, q_out, k_out, fp.RotaryTable(d, base=1e5), w, None)
+    p = pos.cpu().numpy().astype(np.float64)
+    for x, out, weight in ((q, q_out, w), (k, k_out, None)):
+        y, size = po.norm_rope(po.f64(x), p, None if weight is None else po.f64(weight), 1e-6, po.turns(d, 1e5)[0])
+        check(out, y, po.norm_rope_tolerance(y, size, out.dtype))
+    assert status() == fp.FATHOM_OK
