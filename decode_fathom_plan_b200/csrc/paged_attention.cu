@@ -39,11 +39,12 @@
 // Each CTA works the list out for itself from the lengths.  A KV head that one
 // CTA has to itself is finished there; the others' parts go to merge_parts_kernel.
 //
-// Measured on B200: 16 sessions of up to 16385 keys, 8 queries of 64 channels a
-// KV head, 75 us (5.3 TB/s, 82% of a plain copy); 64 of up to 2048 keys of 128,
-// 74 us (5.5 TB/s); one of 131072 keys 90 us (5.95 TB/s, 92%); one of 2047 keys
-// 7.9 us with the joining, in nine dependent loads.  What bounds it is loads in
-// flight, 4 KB or more for each of 16 to 20 warps a multiprocessor.
+// Measured on B200, a call among others, on several GPUs: 16 sessions of up to
+// 16385 keys, 8 queries of 64 channels a KV head, 75 to 80 us (77 to 81% of a
+// plain copy); one of 131072 keys 90 us (92%); one of 2047 keys 8.3 us with the
+// joining, in nine dependent loads.  The kernel alone on 64 sequences of up to
+// 2048 keys of 128: 73.5 us (5.5 TB/s).  Memory bounds it; it has 4 KB or more in
+// flight for each of 16 to 20 warps a multiprocessor.
 #include <math.h>
 
 #include <algorithm>

@@ -24,12 +24,13 @@
 // by more than 2^8.  The parts of all runs are joined with the sequences' own
 // keys by merge_parts_kernel.
 //
-// Measured on B200: 256 rows of 8 KV heads over 32768 keys of 128 channels 43
-// us (floor 21 us by either bound), the tensor pipe 46% busy.  A step of both
-// slots takes 1800 cycles; its products alone would take 1280, as those of 64
-// keys read 6 KB of shared memory for 32 cycles of work.  The first product
-// with V is issued after 7900 cycles: page table, copies, scores and softmax
-// in turn.
+// Measured on B200: 256 rows of 8 KV heads over 32768 keys of 128 channels 45
+// to 48 us alone (floor 21 us by either bound), the tensor pipe 42 to 46% busy;
+// with 64 sequences' own keys behind them and the joining 133 to 138 us a call.
+// A step of both slots takes 1800 cycles; its products alone would take 1280, as
+// those of 64 keys read 6 KB of shared memory for 32 cycles of work.  The first
+// product with V is issued after 7900 cycles: page table, copies, scores and
+// softmax in turn.
 //
 // Every wait has a time limit.  Where one runs out all warps stop at their next
 // one; when they are together again the CTA waits (with a limit) for every copy

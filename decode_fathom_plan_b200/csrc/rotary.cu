@@ -25,9 +25,11 @@
 // (CTAs of 256 threads: 4 to 10% slower; a register more per thread and a
 // quarter fewer warps: 8% slower).  A CTA's rows are all queries, all keys or
 // all values, so that what describes them is uniform (mixed: 20% slower).
-// Measured on B200: a 32768-token prompt of 32 + 8 heads of 128, bf16 to bf16
-// and float32, 127 us (5.8 TB/s, 90% of a plain copy); its keys and values into
-// pages of 32, 52 us (5.2 TB/s, 80%); one token 2.7 us.
+// Measured on B200, a call among others, on several GPUs: a 32768-token prompt
+// of 32 + 8 heads of 128, bf16 to bf16 and float32, 134 to 142 us (80 to 85% of
+// a plain copy), float32 throughout 207 us; its keys and values into pages of
+// 32, 52 us (80%); one token 3.4 us.  An element at a time (rows off their 16
+// bytes, rotated widths that are no multiple of 16) the prompt takes 420 us.
 #include <algorithm>
 
 #include "paged.cuh"
