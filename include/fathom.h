@@ -557,15 +557,16 @@ size_t fathom_paged_attention_workspace_bytes(const fathom_kv_cache *cache, int3
  * if not 0, below prefix_len sets FATHOM_ERR_INVALID_ARG in the device status,
  * and that sequence gets zeros.  A key on a bad page is skipped (one of a
  * shared prefix may take part with a K and V of zeros instead).
- * q, out: rows of n_seqs tokens with G*n_kv_heads heads, in the cache's type,
- * 16-byte aligned, strides positive multiples of 8, n_seqs at most 65535; G
- * 1..8.  slopes: device float32
- * [G*n_kv_heads].  Scores, softmax and sums are float32; for its product with
- * V, which is accumulated in float32, a probability is rounded to the cache's
- * type: float16 once, to 11 bits and 2^-32 of the row's largest; bfloat16 to two
- * terms (16 bits), but over a shared prefix to one (8 bits) where the batch's
- * repeated reads of it, 4 * head_dim * n_kv_heads * prefix_len * (n_seqs - 1)
- * bytes, pass 8 MiB.  prefix_len 0 keeps both terms.  workspace: device memory that no other call in flight uses. */
+ * q, out: rows of n_seqs (1 to 65535) tokens with G*n_kv_heads heads, in the
+ * cache's type, 16-byte aligned, strides positive multiples of 8; G 1..8.
+ * slopes: device float32 [G*n_kv_heads].  Scores, softmax and sums are float32;
+ * for its product with V, which is accumulated in float32, a probability is
+ * rounded to the cache's type: float16 once, to 11 bits or 2^-32 of the row's
+ * largest; bfloat16 to two terms (16 bits), but over a shared prefix to one
+ * (8 bits) where the batch's repeated reads of it,
+ * 4 * head_dim * n_kv_heads * prefix_len * (n_seqs - 1) bytes, are 8 MiB or
+ * more (prefix_len 0 keeps both terms).  Equal inputs give equal outputs, bit
+ * for bit.  workspace: device memory that no other call in flight uses. */
 fathom_status fathom_paged_attention(const fathom_kv_cache *cache, const fathom_rows *q,
                                      const int32_t *page_table, int32_t table_stride,
                                      const int32_t *seq_lens, int32_t n_seqs, int32_t max_len,
